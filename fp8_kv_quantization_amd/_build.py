@@ -1,9 +1,12 @@
-"""Builds libkvstore.so in-tree with hipcc for gfx950, and its CPython
-binding (_kvstore_py, gcc, linked against libkvstore.so)."""
+"""Builds libkvstore.so in-tree with hipcc for gfx950 (its objects are compiled
+side by side), and its CPython binding (_kvstore_py, gcc, linked against
+libkvstore.so)."""
 from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,8 +27,27 @@ FLAGS = [
 ]
 
 
-def command(out: str = LIB, extra=()) -> list:
-    return [HIPCC, *FLAGS, *extra, "-I", os.path.join(ROOT, "include"), SRC, "-o", out]
+def objects() -> list:
+    """(source, extra flags, object name) of every object of the library: the
+    stores, loads and host side, and the attention kernels once per source
+    type and cache format."""
+    csrc = os.path.join(PKG, "csrc")
+    objs = [(os.path.join(csrc, "libkvstore.hip"), [], "libkvstore.o")]
+    for fp16 in (0, 1):
+        for fmt in range(4):
+            objs.append((os.path.join(csrc, "attention_split.hip"),
+                         [f"-DKVATTN_FP16={fp16}", f"-DKVATTN_FMT={fmt}"],
+                         f"attention_split_{fp16}_{fmt}.o"))
+    return objs
+
+
+def command(src: str, out: str, extra=()) -> list:
+    return [HIPCC, *[f for f in FLAGS if f != "-shared"], *extra,
+            "-I", os.path.join(ROOT, "include"), "-c", src, "-o", out]
+
+
+def link_command(objs, out: str = LIB) -> list:
+    return [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", out]
 
 
 def binding_command(out: str = PY_EXT) -> list:
@@ -49,8 +71,12 @@ def _run(cmd, out, what, verbose):
 
 def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
     """Compile the HIP library and, for the in-tree library, the CPython
-    binding (always; a few seconds).  Writes atomically."""
-    _run(command(out, extra), out, "hipcc", verbose)
+    binding (always).  Writes atomically."""
+    with tempfile.TemporaryDirectory() as tmp:
+        made = [(src, os.path.join(tmp, name), [*flags, *extra]) for src, flags, name in objects()]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda m: _run(command(m[0], m[1], m[2]), m[1], "hipcc", verbose), made))
+        _run(link_command([m[1] for m in made], out), out, "hipcc (link)", verbose)
     if out == LIB:
         _run(binding_command(), PY_EXT, "gcc (binding)", verbose)
     return out

@@ -1,0 +1,220 @@
+// Device code that the attention kernels share: which rows and keys a block
+// works on, and the conversions of cached values to 16 bits.
+#pragma once
+
+#include "attention.h"
+
+namespace kvattn {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ void report(unsigned long long* flag, uint32_t token) {
+  unsigned long long seen = 0xFFFFFFFFull;
+  for (;;) {   // ends: every failed exchange means that another report landed
+    const uint32_t first = (uint32_t)seen < token ? (uint32_t)seen : token;
+    const uint32_t count = (uint32_t)(seen >> 32);
+    const unsigned long long next =
+        ((unsigned long long)(count == 0xFFFFFFFFu ? count : count + 1u) << 32) | first;
+    const unsigned long long prev = atomicCAS(flag, seen, next);
+    if (prev == seen) return;
+    seen = prev;
+  }
+}
+
+__device__ __forceinline__ int32_t clamp_row(const Params& p, int32_t r) {
+  return r < 0 ? 0 : (uint32_t)r > p.tokens ? (int32_t)p.tokens : r;
+}
+
+// Tile slots: sequence b of new-token rows [c_b, c_{b+1}) owns the slots from
+// c_b * group / rows + b on.  These starts grow by at least one per sequence
+// and leave it room for all its tiles (floor(x + y) >= floor(x) + ceil(y) - 1),
+// so a block finds its sequence from cu_q alone, with no prefix sums; slots
+// beyond a sequence's tiles hold nothing.
+__device__ __forceinline__ int64_t slot_start(const Params& p, uint32_t b, uint32_t rows) {
+  return (int64_t)clamp_row(p, p.cu_q[b]) * p.group / rows + b;
+}
+
+// A tile: `rows` (token, head in group) pairs of one sequence, and its keys as
+// steps of kStep: first those of the first tokens, then those of the window.
+struct Tile {
+  uint32_t seq;
+  int32_t token0;      // row of q of the tile's first token
+  int32_t row0, rows;  // rows [row0, row0 + rows) of the sequence's new tokens * group
+  int32_t first_pos;   // position of the sequence's first new token
+  int32_t p_lo, p_hi;  // positions of the tile's first and last token
+  int32_t end;         // keys are [0, end)
+  int32_t low;         // first key of any row's window
+  int32_t sink_steps;  // steps [0, sink_steps) start at key 0
+  int32_t low_step;    // step sink_steps starts at key low_step * kStep
+  int32_t steps;
+};
+
+// Steps of a split of the tile, and how many splits that makes (at least one).
+// A tile with more steps than the host planned for gets longer splits.
+__device__ __forceinline__ int32_t split_steps(const Params& p, const Tile& t, int32_t* n_splits) {
+  const int32_t even = (t.steps + p.splits - 1) / p.splits;
+  const int32_t chunk = even > p.chunk_steps ? even : p.chunk_steps;
+  *n_splits = t.steps <= chunk ? 1 : (t.steps + chunk - 1) / chunk;
+  return chunk;
+}
+
+__device__ __forceinline__ int32_t step_key(const Tile& t, int32_t step) {
+  return (step < t.sink_steps ? step : step - t.sink_steps + t.low_step) * kStep;
+}
+
+// False where the slot holds no tile.  All lanes of a wave call it together.
+__device__ __forceinline__ bool tile_of(const Params& p, uint32_t slot, int32_t tile_rows,
+                                        Tile* t) {
+  int32_t begin, n;
+  int32_t index;   // of the tile in its sequence
+  if (p.cu_q == nullptr) {
+    const uint32_t per = (p.group + tile_rows - 1) / tile_rows;
+    t->seq = slot / per;
+    index = slot - t->seq * per;
+    begin = t->seq;
+    n = 1;
+  } else {
+    // The last sequence whose start is at most `slot`, by 64-way search: starts
+    // increase, so the lanes that hold one at most `slot` are the first ones.
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t lo = 0, size = p.seqs;
+    while (size > 0) {
+      const uint32_t stride = (size + 63) / 64;
+      const uint32_t b = lo + lane * stride;
+      const bool at_most = lane * stride < size && slot_start(p, b, tile_rows) <= slot;
+      const uint32_t k = __popcll(__ballot(at_most));
+      if (k == 0) return false;   // before the first sequence
+      lo += (k - 1) * stride;
+      const uint32_t rest = size - (k - 1) * stride;
+      size = stride == 1 ? 0 : (rest < stride ? rest : stride);
+    }
+    t->seq = lo;
+    begin = clamp_row(p, p.cu_q[lo]);
+    n = clamp_row(p, p.cu_q[lo + 1]) - begin;
+    const int64_t i = (int64_t)slot - slot_start(p, lo, tile_rows);
+    if (n <= 0 || i * tile_rows >= (int64_t)n * p.group) return false;
+    index = (int32_t)i;
+  }
+  int32_t len = p.seq_lens[t->seq];
+  len = len < 0 ? 0 : len > p.max_keys ? p.max_keys : len;
+  const int64_t all = (int64_t)n * p.group;
+  const int64_t r0 = (int64_t)index * tile_rows;
+  // rows of a sequence stay below 2^31: checked on the host (tokens * group)
+  t->row0 = (int32_t)r0;
+  t->rows = (int32_t)(all - r0 < tile_rows ? all - r0 : tile_rows);
+  t->token0 = begin;
+  t->first_pos = len - n;
+  t->p_lo = t->first_pos + t->row0 / (int32_t)p.group;
+  t->p_hi = t->first_pos + (t->row0 + t->rows - 1) / (int32_t)p.group;
+  t->end = t->p_hi + 1;   // p_hi < len
+  if (t->end <= 0) {      // positions before the sequence: no keys
+    t->end = t->low = t->sink_steps = t->low_step = t->steps = 0;
+    return true;
+  }
+  const int64_t low = (int64_t)t->p_lo - p.window + 1;
+  t->low = low > 0 ? (int32_t)low : 0;
+  t->low_step = t->low / kStep;
+  const int32_t sinks = p.sinks < t->low_step * kStep ? p.sinks : t->low_step * kStep;
+  t->sink_steps = (sinks + kStep - 1) / kStep;
+  t->steps = t->sink_steps + (t->end + kStep - 1) / kStep - t->low_step;
+  return true;
+}
+
+// Conversions of cached codes to pairs of the source type; values are exact
+// (code * 2^e) as far as the type's range goes.
+template <bool kFp16, int kFmt>
+__device__ __forceinline__ uint32_t pair_of8(uint32_t w, float scale, bool hi) {
+  if constexpr (kFp16) {
+    h16x2 r;
+    if constexpr (kFmt == kFmtE4M3)
+      r = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, true)
+             : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, false);
+    else
+      r = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, scale, true)
+             : __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, scale, false);
+    return __builtin_bit_cast(uint32_t, r);
+  } else {
+    b16x2 r;
+    if constexpr (kFmt == kFmtE4M3)
+      r = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true)
+             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+    else
+      r = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true)
+             : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false);
+    return __builtin_bit_cast(uint32_t, r);
+  }
+}
+
+template <bool kFp16, int kSel>
+__device__ __forceinline__ uint32_t pair_of4(uint32_t w, float scale) {
+  if constexpr (kFp16)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, kSel));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, kSel));
+}
+
+// Eight cached elements -> eight 16-bit values.  `w`: 16 bytes (16 bits), the
+// first 8 (FP8) or 4 (4 bits) of them.
+template <bool kFp16, int kFmt>
+__device__ __forceinline__ u32x4 values8(uint32_t w0, uint32_t w1, float scale) {
+  if constexpr (kFmt == kFmtFp4)
+    return u32x4{pair_of4<kFp16, 0>(w0, scale), pair_of4<kFp16, 1>(w0, scale),
+                 pair_of4<kFp16, 2>(w0, scale), pair_of4<kFp16, 3>(w0, scale)};
+  else
+    return u32x4{pair_of8<kFp16, kFmt>(w0, scale, false), pair_of8<kFp16, kFmt>(w0, scale, true),
+                 pair_of8<kFp16, kFmt>(w1, scale, false), pair_of8<kFp16, kFmt>(w1, scale, true)};
+}
+
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (kFp16) return __builtin_bit_cast(uint32_t, h16x2{(_Float16)a, (_Float16)b});
+  else return __builtin_bit_cast(uint32_t, b16x2{(__bf16)a, (__bf16)b});
+}
+
+template <bool kFp16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (kFp16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, a),
+                                                  __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, a),
+                                                   __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+}
+
+// Four rows' 16-bit values of one column: lane i of a group of 16 addresses row
+// i / 4, columns 4 * (i % 4) ... + 3 of a 4 x 16 block in LDS, and gets column
+// i of its four rows.
+__device__ __forceinline__ u32x2 read_column4(uint8_t* at) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+}
+
+// Page and offset of a key.
+__device__ __forceinline__ void key_page(const Params& p, int32_t key, int32_t* page,
+                                         int32_t* off) {
+  if (p.page_shift >= 0) {
+    *page = key >> p.page_shift;
+    *off = key & (p.page_size - 1);
+  } else {
+    *page = (int32_t)((uint32_t)key / (uint32_t)p.page_size);
+    *off = key - *page * p.page_size;
+  }
+}
+
+// What a row of new tokens sees.
+__device__ __forceinline__ bool sees(const Params& p, int32_t pos, int32_t key) {
+  return key <= pos && (pos - key < p.window || key < p.sinks);
+}
+
+}  // namespace kvattn
