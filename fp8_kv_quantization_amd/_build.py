@@ -35,9 +35,10 @@ def objects() -> list:
     objs = [(os.path.join(csrc, "libkvstore.hip"), [], "libkvstore.o")]
     for fp16 in (0, 1):
         for fmt in range(4):
-            objs.append((os.path.join(csrc, "attention_split.hip"),
-                         [f"-DKVATTN_FP16={fp16}", f"-DKVATTN_FMT={fmt}"],
-                         f"attention_split_{fp16}_{fmt}.o"))
+            for kind in ("split", "tile"):
+                objs.append((os.path.join(csrc, f"attention_{kind}.hip"),
+                             [f"-DKVATTN_FP16={fp16}", f"-DKVATTN_FMT={fmt}"],
+                             f"attention_{kind}_{fp16}_{fmt}.o"))
     return objs
 
 

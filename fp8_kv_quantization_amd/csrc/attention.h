@@ -44,12 +44,15 @@ struct Params {
   int32_t splits;          // splits that the workspace has room for
 };
 
-// Rows (token, head) of a tile and keys of a step, by kernel.
-constexpr int kStep = 32;
+// Keys of a step of the split kernel and of the tile kernel, rows of a tile of
+// the latter.
+constexpr int kSplitStep = 32;
+constexpr int kTileStep = 64;
+constexpr int kTileRows = 128;
 
-// One per (source type, format): the split kernel for tiles of 16 * nr rows.
-// Each returns a KVSTORE_* status.
-typedef int (*SplitLaunch)(const Params& p, int padded_dim, int nr, hipStream_t stream);
+// One per (source type, format); each returns a KVSTORE_* status.
+typedef int (*Launch)(const Params& p, int padded_dim, int nr, hipStream_t stream);
+// The split kernel for tiles of 16 * nr rows; the tile kernel (nr is not read).
 int launch_split_bf16_0(const Params&, int, int, hipStream_t);
 int launch_split_bf16_1(const Params&, int, int, hipStream_t);
 int launch_split_bf16_2(const Params&, int, int, hipStream_t);
@@ -58,5 +61,14 @@ int launch_split_fp16_0(const Params&, int, int, hipStream_t);
 int launch_split_fp16_1(const Params&, int, int, hipStream_t);
 int launch_split_fp16_2(const Params&, int, int, hipStream_t);
 int launch_split_fp16_3(const Params&, int, int, hipStream_t);
+
+int launch_tile_bf16_0(const Params&, int, int, hipStream_t);
+int launch_tile_bf16_1(const Params&, int, int, hipStream_t);
+int launch_tile_bf16_2(const Params&, int, int, hipStream_t);
+int launch_tile_bf16_3(const Params&, int, int, hipStream_t);
+int launch_tile_fp16_0(const Params&, int, int, hipStream_t);
+int launch_tile_fp16_1(const Params&, int, int, hipStream_t);
+int launch_tile_fp16_2(const Params&, int, int, hipStream_t);
+int launch_tile_fp16_3(const Params&, int, int, hipStream_t);
 
 }  // namespace kvattn

@@ -47,6 +47,7 @@ __device__ __forceinline__ int64_t slot_start(const Params& p, uint32_t b, uint3
 
 // A tile: `rows` (token, head in group) pairs of one sequence, and its keys as
 // steps of kStep: first those of the first tokens, then those of the window.
+template <int kStep>
 struct Tile {
   uint32_t seq;
   int32_t token0;      // row of q of the tile's first token
@@ -58,24 +59,29 @@ struct Tile {
   int32_t sink_steps;  // steps [0, sink_steps) start at key 0
   int32_t low_step;    // step sink_steps starts at key low_step * kStep
   int32_t steps;
+
+  __device__ __forceinline__ int32_t key_of(int32_t step) const {
+    return (step < sink_steps ? step : step - sink_steps + low_step) * kStep;
+  }
 };
 
 // Steps of a split of the tile, and how many splits that makes (at least one).
 // A tile with more steps than the host planned for gets longer splits.
-__device__ __forceinline__ int32_t split_steps(const Params& p, const Tile& t, int32_t* n_splits) {
+template <int kStep>
+__device__ __forceinline__ int32_t split_steps(const Params& p, const Tile<kStep>& t,
+                                               int32_t* n_splits) {
   const int32_t even = (t.steps + p.splits - 1) / p.splits;
   const int32_t chunk = even > p.chunk_steps ? even : p.chunk_steps;
   *n_splits = t.steps <= chunk ? 1 : (t.steps + chunk - 1) / chunk;
   return chunk;
 }
 
-__device__ __forceinline__ int32_t step_key(const Tile& t, int32_t step) {
-  return (step < t.sink_steps ? step : step - t.sink_steps + t.low_step) * kStep;
-}
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // False where the slot holds no tile.  All lanes of a wave call it together.
+template <int kStep>
 __device__ __forceinline__ bool tile_of(const Params& p, uint32_t slot, int32_t tile_rows,
-                                        Tile* t) {
+                                        Tile<kStep>* t) {
   int32_t begin, n;
   int32_t index;   // of the tile in its sequence
   if (p.cu_q == nullptr) {
@@ -95,18 +101,18 @@ __device__ __forceinline__ bool tile_of(const Params& p, uint32_t slot, int32_t 
       const bool at_most = lane * stride < size && slot_start(p, b, tile_rows) <= slot;
       const uint32_t k = __popcll(__ballot(at_most));
       if (k == 0) return false;   // before the first sequence
-      lo += (k - 1) * stride;
+      lo = uniform(lo + (k - 1) * stride);
       const uint32_t rest = size - (k - 1) * stride;
       size = stride == 1 ? 0 : (rest < stride ? rest : stride);
     }
     t->seq = lo;
-    begin = clamp_row(p, p.cu_q[lo]);
-    n = clamp_row(p, p.cu_q[lo + 1]) - begin;
+    begin = uniform(clamp_row(p, p.cu_q[lo]));
+    n = uniform(clamp_row(p, p.cu_q[lo + 1])) - begin;
     const int64_t i = (int64_t)slot - slot_start(p, lo, tile_rows);
     if (n <= 0 || i * tile_rows >= (int64_t)n * p.group) return false;
     index = (int32_t)i;
   }
-  int32_t len = p.seq_lens[t->seq];
+  int32_t len = uniform(p.seq_lens[t->seq]);
   len = len < 0 ? 0 : len > p.max_keys ? p.max_keys : len;
   const int64_t all = (int64_t)n * p.group;
   const int64_t r0 = (int64_t)index * tile_rows;
@@ -183,6 +189,16 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
 }
 
 template <bool kFp16>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (kFp16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h16x8, a),
+                                                  __builtin_bit_cast(h16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a),
+                                                   __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+}
+
+template <bool kFp16>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   if constexpr (kFp16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8, a),
@@ -215,6 +231,56 @@ __device__ __forceinline__ void key_page(const Params& p, int32_t key, int32_t* 
 // What a row of new tokens sees.
 __device__ __forceinline__ bool sees(const Params& p, int32_t pos, int32_t key) {
   return key <= pos && (pos - key < p.window || key < p.sinks);
+}
+
+// A row of a tile: its token (row of q), q head, and index among all rows.
+struct Row {
+  int64_t token;
+  int32_t head;
+  int64_t index;
+};
+template <int kStep>
+__device__ __forceinline__ Row row_of(const Params& p, const Tile<kStep>& t, uint32_t kv_head,
+                                      int32_t r) {
+  const int32_t row = t.row0 + r, tok = row / (int32_t)p.group;
+  Row x;
+  x.token = t.token0 + tok;
+  x.head = kv_head * p.group + (row - tok * (int32_t)p.group);
+  x.index = x.token * (int64_t)(p.kv_heads * p.group) + x.head;
+  return x;
+}
+
+// Joins the splits of each row: 16 threads per row.
+template <bool kFp16, int kStep>
+__device__ __forceinline__ void join_splits(const Params& p, int32_t tile_rows, float v_scale) {
+  const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
+  Tile<kStep> t;
+  if (!tile_of(p, slot, tile_rows, &t)) return;
+  int32_t n_splits;
+  split_steps(p, t, &n_splits);
+  if (n_splits == 1) return;
+  for (int r = threadIdx.x >> 4; r < t.rows; r += 16) {
+    const Row x = row_of(p, t, head, r);
+    const int64_t at = x.index * p.splits;
+    float top = kNegInf, sum = 0.0f;
+    for (int i = 0; i < n_splits; ++i) top = fmaxf(top, p.ws_ml[2 * (at + i)]);
+    for (int i = 0; i < n_splits; ++i) {
+      const float mi = p.ws_ml[2 * (at + i)];
+      if (mi != kNegInf) sum += p.ws_ml[2 * (at + i) + 1] * __builtin_amdgcn_exp2f(mi - top);
+    }
+    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+    for (int d = (threadIdx.x & 15) * 4; d < p.dim; d += 64) {
+      f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < n_splits; ++i) {
+        const float mi = p.ws_ml[2 * (at + i)];
+        if (mi == kNegInf) continue;
+        y += *reinterpret_cast<const f32x4*>(p.ws_o + (at + i) * p.dim + d) *
+             __builtin_amdgcn_exp2f(mi - top);
+      }
+      *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
+          u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
+    }
+  }
 }
 
 }  // namespace kvattn

@@ -21,7 +21,7 @@ unsigned long long* error_flag() {
 }
 
 struct AttentionPlan {
-  int nr;               // 16-row groups of a tile
+  int nr;               // 16-row groups of a split tile; 0: the tile kernel
   int padded_dim;
   uint32_t tile_slots;
   int32_t max_keys;
@@ -51,9 +51,10 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t group = a.q_heads / c.num_heads;
   const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q == 0 || a.max_q > a.tokens ? a.tokens : a.max_q;
   const int64_t rows = max_q * group;
-  plan->nr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  plan->nr = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+  const int64_t step = plan->nr > 0 ? kvattn::kSplitStep : kvattn::kTileStep;
   plan->padded_dim = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-  const int64_t tile = 16 * plan->nr;
+  const int64_t tile = plan->nr > 0 ? 16 * plan->nr : kvattn::kTileRows;
   const int64_t slots = a.cu_q == nullptr ? a.seqs * ceil_div(group, tile)
                                           : (int64_t)a.tokens * group / tile + a.seqs;
   if (slots * c.num_heads > (int64_t(1) << 24)) return KVSTORE_ERR_SHAPE;   // 2^32 work-items
@@ -63,10 +64,10 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   int64_t keys = a.max_len > 0 && a.max_len < plan->max_keys ? a.max_len : plan->max_keys;
   if (a.window > 0) {
     const int64_t span = a.window + (max_q < ceil_div(tile, group) ? max_q : ceil_div(tile, group)) +
-                         a.sinks + 2 * kvattn::kStep;
+                         a.sinks + 2 * step;
     if (a.window < keys && a.sinks < keys && span < keys) keys = span;
   }
-  const int64_t steps = ceil_div(keys, kvattn::kStep);
+  const int64_t steps = ceil_div(keys, step);
   const int64_t tiles = a.cu_q == nullptr ? slots
                         : rows <= tile    ? (int64_t)a.seqs
                                           : (int64_t)a.tokens * group / tile + a.seqs / 2;
@@ -166,12 +167,17 @@ int kvstore_attention_paged(const kvstore_attention_args* args, const kvstore_pa
   p.scale_kind = c.scale_kind;
   p.chunk_steps = plan.chunk_steps;
   p.splits = plan.splits;
-  static const kvattn::SplitLaunch split[2][4] = {
+  static const kvattn::Launch split[2][4] = {
       {kvattn::launch_split_bf16_0, kvattn::launch_split_bf16_1, kvattn::launch_split_bf16_2,
        kvattn::launch_split_bf16_3},
       {kvattn::launch_split_fp16_0, kvattn::launch_split_fp16_1, kvattn::launch_split_fp16_2,
        kvattn::launch_split_fp16_3}};
-  return split[fp16][fmt](p, plan.padded_dim, plan.nr, stream);
+  static const kvattn::Launch tile[2][4] = {
+      {kvattn::launch_tile_bf16_0, kvattn::launch_tile_bf16_1, kvattn::launch_tile_bf16_2,
+       kvattn::launch_tile_bf16_3},
+      {kvattn::launch_tile_fp16_0, kvattn::launch_tile_fp16_1, kvattn::launch_tile_fp16_2,
+       kvattn::launch_tile_fp16_3}};
+  return (plan.nr > 0 ? split : tile)[fp16][fmt](p, plan.padded_dim, plan.nr, stream);
 }
 
 }  // extern "C"

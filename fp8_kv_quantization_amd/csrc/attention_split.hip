@@ -31,6 +31,7 @@ constexpr int kWaves = 4;
 constexpr bool kFp16 = KVATTN_FP16 != 0;
 constexpr int kFmt = KVATTN_FMT;
 constexpr float kLazy = 8.0f;
+constexpr int kStep = kSplitStep;
 
 template <int kDim>
 struct Shape {
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
   const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const uint32_t g = lane >> 4, c16 = lane & 15;
-  Tile t;
+  Tile<kStep> t;
   if (!tile_of(p, slot, kTileRows, &t)) return;
   int32_t n_splits;
   const int32_t chunk = split_steps(p, t, &n_splits);
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   // The page of this lane's key of a step (lanes l and l + 32 take key l): -2
   // where no row of the tile sees the key.
   auto page_id = [&](int32_t step) -> int32_t {
-    const int32_t key = step_key(t, step) + kk;
+    const int32_t key = t.key_of(step) + kk;
     if (key >= t.end || (key < t.low && key >= p.sinks)) return -2;
     int32_t page, off;
     key_page(p, key, &page, &off);
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 
   // Places the step's keys and issues their loads.
   auto load_step = [&](int32_t step, int32_t page) {
-    const int32_t key = step_key(t, step) + kk;
+    const int32_t key = t.key_of(step) + kk;
     int32_t ignore, off;
     key_page(p, key, &ignore, &off);
     const bool there = page >= 0 && page < p.num_pages;
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     if (step + kWaves < s_end) page_next = page_id(step + kWaves);
   }
   for (; step < s_end; step += kWaves) {
-    const int32_t key0 = step_key(t, step);
+    const int32_t key0 = t.key_of(step);
     const uint32_t ok_now = ok;
     store_v();
 
@@ -403,7 +404,6 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     }
   }
   __syncthreads();
-  const int32_t q_heads = (int32_t)(p.kv_heads * p.group);
 #pragma unroll
   for (int n = 0; n < kNr; ++n) {
     if (n > 0) __syncthreads();
@@ -432,11 +432,8 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         const float mi = s_m[i][n * 16 + r];
         row_l += mi == kNegInf ? 0.0f : s_l[i][n * 16 + r] * __builtin_amdgcn_exp2f(mi - row_top);
       }
-      const int32_t row = t.row0 + n * 16 + r;
-      const int32_t tok = row / (int32_t)p.group;
-      const int64_t token = t.token0 + tok;
-      const int32_t qh = head * p.group + (row - tok * (int32_t)p.group);
-      const int64_t at = (token * q_heads + qh) * p.splits + blockIdx.y;
+      const Row x = row_of(p, t, head, n * 16 + r);
+      const int64_t at = x.index * p.splits + blockIdx.y;
       const float inv = row_l == 0.0f ? 0.0f : v_scale / row_l;
 #pragma unroll
       for (int d = part * 4; d < kDim; d += 64) {
@@ -447,7 +444,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
                                                r * S::kStrideO + d);
         if (d >= p.dim) continue;
         if (n_splits == 1) {
-          *reinterpret_cast<u32x2*>(p.out + token * p.o_token + (int64_t)qh * p.o_head + 2 * d) =
+          *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
               u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
         } else {
           *reinterpret_cast<f32x4*>(p.ws_o + at * p.dim + d) = y;
@@ -461,44 +458,12 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   }
 }
 
-// Joins the splits of each row: 16 threads per row.
 template <int kNr>
 __global__ __launch_bounds__(256) void kvattn_join_kernel(const Params p) {
-  constexpr int kTileRows = 16 * kNr;
-  const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
-  Tile t;
-  if (!tile_of(p, slot, kTileRows, &t)) return;
-  int32_t n_splits;
-  split_steps(p, t, &n_splits);
-  if (n_splits == 1) return;
-  float v_scale = 1.0f;
-  if ((kFmt == kFmtE4M3 || kFmt == kFmtE5M2) && p.scale_kind == KVATTN_TENSOR && p.v.scales)
-    v_scale = *reinterpret_cast<const float*>(p.v.scales);
-  const int32_t q_heads = (int32_t)(p.kv_heads * p.group);
-  for (int r = threadIdx.x >> 4; r < t.rows; r += 16) {
-    const int32_t row = t.row0 + r;
-    const int32_t tok = row / (int32_t)p.group;
-    const int64_t token = t.token0 + tok;
-    const int32_t qh = head * p.group + (row - tok * (int32_t)p.group);
-    const int64_t at = (token * q_heads + qh) * p.splits;
-    float top = kNegInf, sum = 0.0f;
-    for (int i = 0; i < n_splits; ++i) top = fmaxf(top, p.ws_ml[2 * (at + i)]);
-    for (int i = 0; i < n_splits; ++i) {
-      const float mi = p.ws_ml[2 * (at + i)];
-      if (mi != kNegInf) sum += p.ws_ml[2 * (at + i) + 1] * __builtin_amdgcn_exp2f(mi - top);
-    }
-    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-    for (int d = (threadIdx.x & 15) * 4; d < p.dim; d += 64) {
-      f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < n_splits; ++i) {
-        const float mi = p.ws_ml[2 * (at + i)];
-        if (mi == kNegInf) continue;
-        y += *reinterpret_cast<const f32x4*>(p.ws_o + (at + i) * p.dim + d) * __builtin_amdgcn_exp2f(mi - top);
-      }
-      *reinterpret_cast<u32x2*>(p.out + token * p.o_token + (int64_t)qh * p.o_head + 2 * d) =
-          u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
-    }
-  }
+  const bool tensor = (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) && p.scale_kind == KVATTN_TENSOR;
+  join_splits<kFp16, kStep>(p, 16 * kNr, tensor && p.v.scales
+                                             ? *reinterpret_cast<const float*>(p.v.scales)
+                                             : 1.0f);
 }
 
 int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) {

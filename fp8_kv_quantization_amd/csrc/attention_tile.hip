@@ -1,0 +1,457 @@
+// Paged attention for many rows (prompts and chunks of them): compiled once per
+// source type and cache format (KVATTN_FP16, KVATTN_FMT).
+//
+//   out = sum_k softmax_k(c q . K_k) V_k over the keys that a row sees.
+//
+// A block owns 128 rows (tokens x q heads of one kv head, so that the heads of
+// a group share the keys that the block reads) and walks their keys in steps of
+// 64; each of its four waves has 32 rows.  K and V go through LDS as 16-bit
+// values, double-buffered: the next step's rows are loaded into registers
+// before a step's products and converted and written behind them, with one
+// barrier a step.  The addresses of a step's rows (page table lookups) are
+// worked out two steps ahead, one key a thread, and handed over through LDS.
+//
+// S^T = K Q^T on 32x32x16 MFMAs; a lane then holds keys of one row only, so the
+// softmax needs one exchange between two lanes, and its weights are in place
+// as the operand P^T of O^T = V^T P^T once the keys of V are taken in the same
+// order: four consecutive ones at a time, by transposing reads.
+//
+// Bound by the matrix cores and the softmax's vector work, which are of equal
+// size at 128 dims (per 64 keys and 32 rows: 1024 cycles of MFMA; 32 exponentials
+// at quarter rate and some 100 other operations, 900 cycles); two waves a SIMD
+// overlap the two.
+#include "attention_device.h"
+#include "kvstore.h"
+
+namespace kvattn {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr bool kFp16 = KVATTN_FP16 != 0;
+constexpr int kFmt = KVATTN_FMT;
+constexpr bool kFp8 = kFmt == kFmtE4M3 || kFmt == kFmtE5M2;
+constexpr float kLazy = 8.0f;
+constexpr int kStep = kTileStep;
+constexpr int kRing = 4;   // steps whose row addresses are kept
+
+template <int kDim>
+struct Shape {
+  static constexpr int kElems = kFmt == kFmt16 ? 8 : kFmt == kFmtFp4 ? 32 : 16;   // of 16 bytes
+  static constexpr int kLanes = kDim / kElems;                 // threads per row
+  static constexpr int kRows = kThreads / kLanes;              // rows per access of the block
+  static constexpr int kLoads = kRows >= kStep ? 1 : kStep / kRows;
+  static constexpr int kStrideK = 2 * kDim + 16;               // bytes of a row in LDS
+  static constexpr int kStrideV = 2 * kDim + 32;
+};
+
+template <int kDim>
+struct Lds {
+  alignas(16) uint8_t k[2][kStep * Shape<kDim>::kStrideK];
+  alignas(16) uint8_t v[2][kStep * Shape<kDim>::kStrideV];
+  const uint8_t* at[kRing][2][kStep];  // K and V rows
+  const uint8_t* scale_at[kFmt == kFmtFp4 ? kRing : 1][2][kFmt == kFmtFp4 ? kStep : 1];
+  alignas(16) float scale[kFp8 ? kRing : 1][2][kFp8 ? kStep : 4];
+  unsigned long long ok[kRing];        // keys that are there
+};
+
+template <int kDim>
+__global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_kernel(const Params p) {
+  typedef Shape<kDim> S;
+  constexpr int kKs = kDim / 16;    // k steps of Q K^T
+  constexpr int kDt = kDim / 32;    // column tiles of O
+  __shared__ Lds<kDim> lds;
+
+  const uint32_t head = blockIdx.x % p.kv_heads;
+  // later tiles of a sequence see more keys: they start first
+  const uint32_t slot = p.tile_slots - 1 - blockIdx.x / p.kv_heads;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const uint32_t half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
+  Tile<kStep> t;
+  if (!tile_of(p, slot, kTileRows, &t)) return;
+  int32_t n_splits;
+  const int32_t chunk = split_steps(p, t, &n_splits);
+  if ((int32_t)blockIdx.y >= n_splits) return;
+  const int32_t s_begin = blockIdx.y * chunk;
+  const int32_t s_end = min(t.steps, s_begin + chunk);
+
+  const bool dyn = kFp8 && p.scale_kind != KVATTN_TENSOR;
+  float c = p.scale2, v_scale = 1.0f;
+  if (kFp8 && !dyn) {
+    if (p.k.scales) c *= *reinterpret_cast<const float*>(p.k.scales);
+    if (p.v.scales) v_scale = *reinterpret_cast<const float*>(p.v.scales);
+  }
+  // The softmax below wants c > 0: a negative one turns the signs of q (exactly),
+  // and for 0 a tiny one does (all weights equal, masked scores still -inf).
+  const uint32_t flip = c < 0.0f ? 0x80008000u : 0u;
+  c = __builtin_fabsf(c);
+  if (c == 0.0f) c = 1e-37f;
+
+  // Q^T operand of this lane's row.
+  const int32_t my_row = w * 32 + c32;
+  u32x4 q[kKs];
+  int32_t pos;
+  {
+    const int32_t row = t.row0 + (my_row < t.rows ? my_row : t.rows - 1);
+    const int32_t tok = row / (int32_t)p.group;
+    pos = t.first_pos + tok;
+    const uint8_t* src = p.q + (int64_t)(t.token0 + tok) * p.q_token +
+                         (int64_t)(head * p.group + (row - tok * (int32_t)p.group)) * p.q_head;
+#pragma unroll
+    for (int ks = 0; ks < kKs; ++ks) {
+      const int d = ks * 16 + half * 8;
+      q[ks] = u32x4{0u, 0u, 0u, 0u};
+      if (d < p.dim) q[ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
+      q[ks] ^= flip;
+    }
+  }
+
+  f32x16 acc[kDt];
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
+  float m = kNegInf, l = 0.0f;   // of this lane's keys; m is the same in lanes l, l ^ 32
+
+  // --- row addresses: threads 0-63 take a step's K rows, 64-127 its V rows ---
+  const int32_t* table = p.table + (int64_t)t.seq * p.table_stride;
+  const bool is_v = w == 1;
+  bool met_bad = false;
+  auto page_id = [&](int32_t step) -> int32_t {   // -2: no row of the tile sees the key
+    if (w > 1 || step >= s_end) return -2;
+    const int32_t key = t.key_of(step) + (int32_t)lane;
+    if (key >= t.end || (key < t.low && key >= p.sinks)) return -2;
+    int32_t page, off;
+    key_page(p, key, &page, &off);
+    return table[page];
+  };
+  auto place = [&](int32_t step, int32_t page) {
+    if (w > 1 || step >= s_end) return;
+    const int32_t key = t.key_of(step) + (int32_t)lane;
+    int32_t ignore, off;
+    key_page(p, key, &ignore, &off);
+    const bool there = page >= 0 && page < p.num_pages;
+    met_bad = met_bad || (page != -2 && !there);
+    const Side& side = is_v ? p.v : p.k;
+    const int r = (step - s_begin) & (kRing - 1);
+    // Slot 0 stands in for keys that are not there: its row is loaded and not used.
+    const int64_t pg = there ? page : 0, of = there ? off : 0;
+    lds.at[r][w][lane] = side.data + pg * side.page + of * side.offset + (int64_t)head * side.head;
+    const int64_t sc_at = pg * side.s_page + of * side.s_offset;
+    if constexpr (kFmt == kFmtFp4)
+      lds.scale_at[r][w][lane] = side.scales + sc_at + (int64_t)head * side.s_head;
+    if constexpr (kFp8) {
+      float sc = 1.0f;
+      if (dyn && there)
+        sc = *reinterpret_cast<const float*>(
+            side.scales + sc_at +
+            (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
+      lds.scale[r][w][lane] = sc;
+    }
+    const unsigned long long ok = __ballot(there);
+    if (tid == 0) lds.ok[r] = ok;
+  };
+
+  // --- rows: global memory -> registers -> LDS ---
+  u32x4 kr[S::kLoads], vr[S::kLoads];
+  uint32_t kb[S::kLoads], vb[S::kLoads];
+  // Threads past the step's rows or the head's dims load a row's start and
+  // write nothing.
+  const int32_t row0 = tid / S::kLanes, col = (tid % S::kLanes) * S::kElems;
+  const bool writes = col < p.dim && row0 < kStep;
+  const int32_t from = writes ? (kFmt == kFmt16 ? 2 * col : kFmt == kFmtFp4 ? col / 2 : col) : 0;
+  auto load_rows = [&](int32_t step) {
+    const int r = (step - s_begin) & (kRing - 1);
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int row = (row0 & (kStep - 1)) + i * S::kRows;
+      kr[i] = *reinterpret_cast<const u32x4*>(lds.at[r][0][row] + from);
+      vr[i] = *reinterpret_cast<const u32x4*>(lds.at[r][1][row] + from);
+      if constexpr (kFmt == kFmtFp4) {
+        kb[i] = lds.scale_at[r][0][row][writes ? col / 32 : 0];
+        vb[i] = lds.scale_at[r][1][row][writes ? col / 32 : 0];
+      }
+    }
+  };
+  auto put = [&](uint8_t* dst, u32x4 x, uint32_t byte, float sc) {
+    if constexpr (kFmt == kFmt16) {
+      *reinterpret_cast<u32x4*>(dst) = x;
+    } else if constexpr (kFmt == kFmtFp4) {
+      const float s4 = __uint_as_float(byte << 23);
+      const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x4*>(dst + 16 * i) = values8<kFp16, kFmt>(e[i], 0, s4);
+    } else {
+      *reinterpret_cast<u32x4*>(dst) = values8<kFp16, kFmt>(x.x, x.y, sc);
+      *reinterpret_cast<u32x4*>(dst + 16) = values8<kFp16, kFmt>(x.z, x.w, sc);
+    }
+  };
+  auto store_rows = [&](int32_t step) {
+    const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
+    const unsigned long long ok = lds.ok[r];
+    if (ok != ~0ull) {   // 0 * V must be 0 for keys that are not there
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) {
+        const bool there = (ok >> (row0 + i * S::kRows)) & 1ull;
+        vr[i] = there ? vr[i] : u32x4{0u, 0u, 0u, 0u};
+        if constexpr (kFmt == kFmtFp4) vb[i] = there ? vb[i] : 127u;
+      }
+    }
+    if (!writes) return;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int row = row0 + i * S::kRows;
+      put(lds.k[b] + row * S::kStrideK + 2 * col, kr[i], kb[i], 1.0f);
+      // V's power of two goes into the values, exactly; its significand into the weights
+      put(lds.v[b] + row * S::kStrideV + 2 * col, vr[i], vb[i],
+          kFp8 ? lds.scale[kFp8 ? r : 0][1][kFp8 ? row : 0] : 1.0f);
+    }
+  };
+
+  if (p.dim < kDim) {   // the columns that no thread writes
+    u32x4* const all = reinterpret_cast<u32x4*>(lds.k[0]);
+    for (uint32_t i = tid; i < (sizeof(lds.k) + sizeof(lds.v)) / 16; i += kThreads)
+      all[i] = u32x4{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  if (s_begin < s_end) {
+    place(s_begin, page_id(s_begin));
+    place(s_begin + 1, page_id(s_begin + 1));
+  }
+  int32_t page_next = page_id(s_begin + 2);
+  __syncthreads();
+  if (s_begin < s_end) {
+    load_rows(s_begin);
+    store_rows(s_begin);
+  }
+  __syncthreads();
+
+  for (int32_t step = s_begin; step < s_end; ++step) {
+    const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
+    const int32_t key0 = t.key_of(step);
+    const bool more = step + 1 < s_end;
+    if (more) load_rows(step + 1);
+    place(step + 2, page_next);
+    page_next = page_id(step + 3);
+
+    // S^T
+    f32x16 s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
+      const uint8_t* kp = lds.k[b] + (h * 32 + c32) * S::kStrideK + half * 16;
+#pragma unroll
+      for (int ks = 0; ks < kKs; ++ks)
+        s[h] = mfma32<kFp16>(*reinterpret_cast<const u32x4*>(kp + ks * 32), q[ks], s[h]);
+    }
+
+    // Key of value i of half h: key0 + 32 h + 8 (i / 4) + 4 half + i % 4.
+    const unsigned long long ok = lds.ok[r];
+    const bool mixed = ok != ~0ull || key0 + kStep - 1 > t.p_lo ||
+                       !(t.p_hi - key0 < p.window || key0 + kStep - 1 < p.sinks);
+    float vm[kFp8 ? 32 : 1];
+    if constexpr (kFp8) {
+      if (dyn) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = 32 * h + 8 * j + 4 * half;
+            const f32x4 ks = *reinterpret_cast<const f32x4*>(&lds.scale[r][0][at]);
+            const f32x4 vs = *reinterpret_cast<const f32x4*>(&lds.scale[r][1][at]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[h][4 * j + i] *= ks[i];
+              vm[16 * h + 4 * j + i] =
+                  __uint_as_float((__float_as_uint(vs[i]) & 0x807FFFFFu) | 0x3F800000u);
+            }
+          }
+      }
+    }
+    uint32_t seen = ~0u;
+    if (mixed) {
+      // sees() of key key0 + 4 half + j, with the differences taken once (and
+      // kept inside the loop: the compiler would carry 32 of them across it)
+      int32_t last = pos - key0 - 4 * (int)half;                       // j <= last
+      int32_t first = last < p.window ? -1 : last - p.window;          // j > first
+      int32_t sink = min(p.sinks - key0, kStep) - 4 * (int)half;       // or j < sink
+      uint32_t ok0 = (uint32_t)(ok >> (4 * half)), ok1 = (uint32_t)((ok >> 32) >> (4 * half));
+      asm volatile("" : "+v"(last), "+v"(first), "+v"(sink), "+v"(ok0), "+v"(ok1));
+      seen = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int32_t jj = 8 * (i >> 2) + (i & 3), j = 32 * h + jj;
+          const bool see = ((h ? ok1 : ok0) >> jj & 1u) != 0 && j <= last && (j > first || j < sink);
+          s[h][i] = see ? s[h][i] : kNegInf;
+          seen |= see ? 1u << (16 * h + i) : 0u;
+        }
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[h][i]);
+    top *= c;
+    if (__ballot(top > m + kLazy || (m == kNegInf && top > kNegInf)) != 0) {
+      const float now = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+      const float f = now == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+    }
+    const float base = m == kNegInf ? 0.0f : -m;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], c, base));
+        l += s[h][i];
+      }
+    if constexpr (kFp8) {
+      if (dyn) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[h][i] = (seen >> (16 * h + i)) & 1u ? s[h][i] * vm[16 * h + i] : 0.0f;
+      }
+    }
+    u32x4 pt[4];   // P^T operands of 16 keys each
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int h = k >> 1, i = 8 * (k & 1);
+      pt[k] = u32x4{pack_pair<kFp16>(s[h][i], s[h][i + 1]), pack_pair<kFp16>(s[h][i + 2], s[h][i + 3]),
+                    pack_pair<kFp16>(s[h][i + 4], s[h][i + 5]), pack_pair<kFp16>(s[h][i + 6], s[h][i + 7])};
+    }
+
+    // O^T += V^T P^T
+    uint8_t* const vp = lds.v[b] + (4 * half + (c16 >> 2)) * S::kStrideV +
+                        (16 * ((lane >> 4) & 1) + 4 * (c16 & 3)) * 2;
+    auto v_operand = [&](int k, int dt) {
+      const u32x2 x = read_column4(vp + (16 * k) * S::kStrideV + dt * 64);
+      const u32x2 y = read_column4(vp + (16 * k + 8) * S::kStrideV + dt * 64);
+      return u32x4{x.x, x.y, y.x, y.y};
+    };
+    bool apart = false;
+    if (mixed && t.p_lo != t.p_hi) {
+      // 0 * V is not 0 where V holds a NaN or an infinity, which must not reach
+      // the rows that do not see it.
+      f32x16 z;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+#pragma unroll 1
+      for (int k = 0; k < 4 * kDt; ++k)
+        z = mfma32<kFp16>(v_operand(k & 3, k >> 2), u32x4{0u, 0u, 0u, 0u}, z);
+      float zz = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) zz += z[i];
+      apart = __ballot(!(zz == 0.0f)) != 0;
+    }
+    if (!apart) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int dt = 0; dt < kDt; ++dt)
+          acc[dt] = mfma32<kFp16>(v_operand(k, dt), pt[k], acc[dt]);
+    } else {
+      // One key at a time, added to the rows that see it.
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll 1
+        for (int j = 0; j < 16; ++j) {
+          const int e = (j & 3) + 4 * (j >> 3);   // element of the operand, in lanes of half (j >> 2) & 1
+          const bool mine = (int)half == ((j >> 2) & 1);
+          const uint32_t keep = mine ? ((e & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+          const uint32_t k0 = e < 2 ? keep : 0u, k1 = (e >> 1) == 1 ? keep : 0u;
+          const uint32_t k2 = (e >> 1) == 2 ? keep : 0u, k3 = e > 5 ? keep : 0u;
+          const u32x4 only = u32x4{k0, k1, k2, k3};
+          const int32_t key = 16 * k + j;
+          const bool see = ((ok >> key) & 1ull) && sees(p, pos, key0 + key);
+          const u32x4 one = pt[k] & only;
+#pragma unroll
+          for (int dt = 0; dt < kDt; ++dt) {
+            f32x16 y;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+            y = mfma32<kFp16>(v_operand(k, dt) & only, one, y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] += see ? y[i] : 0.0f;
+            __builtin_amdgcn_sched_barrier(0);   // one at a time: this is the rare path
+          }
+        }
+      }
+    }
+
+    if (more) store_rows(step + 1);
+    __syncthreads();
+  }
+  if (__ballot(met_bad) != 0 && tid == 0 && head == 0)
+    report(p.flag, (uint32_t)(t.token0 + t.row0 / (int32_t)p.group));
+
+  l += __shfl_xor(l, 32);
+  if (my_row >= t.rows) return;
+  const Row x = row_of(p, t, head, my_row);
+  const int64_t at = x.index * p.splits + blockIdx.y;
+  const float inv = l == 0.0f ? 0.0f : v_scale / l;
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = dt * 32 + 8 * j + 4 * half;
+      if (d >= p.dim) continue;
+      const f32x4 y = f32x4{acc[dt][4 * j], acc[dt][4 * j + 1], acc[dt][4 * j + 2], acc[dt][4 * j + 3]};
+      if (n_splits == 1)
+        *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
+            u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
+      else
+        *reinterpret_cast<f32x4*>(p.ws_o + at * p.dim + d) = y;
+    }
+  if (n_splits > 1 && half == 0) {
+    p.ws_ml[2 * at] = m;
+    p.ws_ml[2 * at + 1] = l;
+  }
+}
+
+__global__ __launch_bounds__(256) void kvattn_join_tiles_kernel(const Params p) {
+  join_splits<kFp16, kStep>(p, kTileRows, kFp8 && p.scale_kind == KVATTN_TENSOR && p.v.scales
+                                              ? *reinterpret_cast<const float*>(p.v.scales)
+                                              : 1.0f);
+}
+
+int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) {
+  Params copy = p;
+  void* argv[] = {&copy};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreads), argv, 0,
+                         stream) == hipSuccess
+             ? KVSTORE_OK
+             : KVSTORE_ERR_HIP;
+}
+
+}  // namespace
+
+#define KVATTN_NAME2(src, fmt) launch_tile_##src##_##fmt
+#define KVATTN_NAME(src, fmt) KVATTN_NAME2(src, fmt)
+#if KVATTN_FP16
+#define KVATTN_SRC fp16
+#else
+#define KVATTN_SRC bf16
+#endif
+
+int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int, hipStream_t stream) {
+  const dim3 grid(p.tile_slots * p.kv_heads, (uint32_t)p.splits);
+  void (*kernel)(Params) = padded_dim == 64    ? kvattn_tile_kernel<64>
+                           : padded_dim == 128 ? kvattn_tile_kernel<128>
+                                               : kvattn_tile_kernel<256>;
+  const int st = run(kernel, grid, p, stream);
+  if (st != KVSTORE_OK || p.splits == 1) return st;
+  return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads), p, stream);
+}
+
+}  // namespace kvattn
