@@ -589,6 +589,62 @@ def load_kv_paged(k_cache, v_cache, cache_loc, k_out, v_out, page_size=16, k_sca
           v_out.data_ptr(), *_input_strides(v_out, H, D), dst, T)
 
 
+def _attention_args(q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks,
+                    sm_scale, page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, out):
+    """Checks attention_paged's arguments; the members of
+    kvstore_attention_args up to the workspace, and those of the cache."""
+    torch = _torch()
+    src = _src_code(q.dtype, "q")
+    cache, H, D, _ = _paged_cache(k_cache, v_cache, page_size, None, q.dtype, k_scale, v_scale,
+                                  k_scale_cache, v_scale_cache, True)
+    if q.dim() != 3 or q.shape[2] != D or q.shape[1] % H:
+        raise ValueError(f"q must be [T, Hq, {D}] with Hq a multiple of {H}")
+    T, Hq = q.shape[0], q.shape[1]
+    if seq_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("seq_lens must be [B] and page_table [B, pages]")
+    B = seq_lens.shape[0]
+    for t in (page_table, seq_lens, cu_q):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("page_table, seq_lens and cu_q must be int32")
+    if (B > 1 and seq_lens.stride(0) != 1) or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("seq_lens and the rows of page_table must be contiguous")
+    if cu_q is None:
+        if T != B:
+            raise ValueError(f"without cu_q every sequence has one token: {T} rows, {B} sequences")
+    elif cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
+        raise ValueError("cu_q must be a contiguous [B + 1]")
+    if window < 0 or sinks < 0 or (max_q is not None and max_q < 0) or (
+            max_len is not None and max_len < 0):
+        raise ValueError("window, sinks, max_q and max_len must not be negative")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
+        raise ValueError("out must have q's shape and dtype")
+    qs = q.stride()
+    os_ = (Hq * D, D, 1) if out is None else out.stride()
+    if qs[2] != 1 or os_[2] != 1:
+        raise ValueError("q and out must have a dim stride of 1")
+    return (q.data_ptr(), None if out is None else out.data_ptr(), qs[0] * 2, qs[1] * 2, os_[0] * 2,
+            os_[1] * 2, src, Hq, None if cu_q is None else cu_q.data_ptr(), T, B, min(max_q or 0, T),
+            page_table.data_ptr(), page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(),
+            max_len or 0, window, sinks, D ** -0.5 if sm_scale is None else sm_scale), cache
+
+
+def _attention_workspace(args, cache) -> int:
+    need = kvstore_attention_workspace((*args, None, 0), cache)
+    if need < 0:
+        raise KVStoreError(need, "kvstore_attention_paged")
+    return need
+
+
+def attention_paged_workspace(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=None,
+                              max_len=None, window=0, sinks=0, page_size=16, k_scale=None,
+                              v_scale=None, k_scale_cache=None, v_scale_cache=None) -> int:
+    """Bytes of workspace that attention_paged needs for these arguments (by
+    their shapes; 0: none)."""
+    return _attention_workspace(*_attention_args(
+        q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks, None,
+        page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, None))
+
+
 def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=None, max_len=None,
                     window=0, sinks=0, sm_scale=None, page_size=16, k_scale=None, v_scale=None,
                     k_scale_cache=None, v_scale_cache=None, out=None, workspace=None, stream=None):
@@ -607,53 +663,18 @@ def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=
     torch = _torch()
     dev = _device_of(q, k_cache, v_cache, page_table, seq_lens, cu_q, k_scale, v_scale,
                      k_scale_cache, v_scale_cache, out, workspace)
-    src = _src_code(q.dtype, "q")
-    cache, H, D, _ = _paged_cache(k_cache, v_cache, page_size, None, q.dtype, k_scale, v_scale,
-                                  k_scale_cache, v_scale_cache, True)
-    if q.dim() != 3 or q.shape[2] != D or q.shape[1] % H:
-        raise ValueError(f"q must be [T, Hq, {D}] with Hq a multiple of {H}")
-    T, Hq = q.shape[0], q.shape[1]
-    B = seq_lens.shape[0]
-    if seq_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("seq_lens must be [B] and page_table [B, pages]")
-    for t in (page_table, seq_lens, cu_q):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("page_table, seq_lens and cu_q must be int32")
-    if (B > 1 and seq_lens.stride(0) != 1) or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("seq_lens and the rows of page_table must be contiguous")
-    if cu_q is None:
-        if T != B:
-            raise ValueError(f"without cu_q every sequence has one token: {T} rows, {B} sequences")
-    elif cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
-        raise ValueError("cu_q must be a contiguous [B + 1]")
-    if window < 0 or sinks < 0 or (max_q is not None and max_q < 0) or (
-            max_len is not None and max_len < 0):
-        raise ValueError("window, sinks, max_q and max_len must not be negative")
     foreign = stream is not None and stream != torch.cuda.current_stream(dev)
-    made = []
     if out is None:
-        out = _on_stream(foreign, stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=dev))
-        made.append(out)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    es = 2
-    qs, os_ = q.stride(), out.stride()
-    if qs[2] != 1 or os_[2] != 1:
-        raise ValueError("q and out must have a dim stride of 1")
-    args = (q.data_ptr(), out.data_ptr(), qs[0] * es, qs[1] * es, os_[0] * es, os_[1] * es, src,
-            Hq, None if cu_q is None else cu_q.data_ptr(), T, B, min(max_q or 0, T),
-            page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-            seq_lens.data_ptr(), max_len or 0, window, sinks,
-            D ** -0.5 if sm_scale is None else sm_scale)
-    need = kvstore_attention_workspace((*args, None, 0), cache)
-    if need < 0:
-        raise KVStoreError(need, "kvstore_attention_paged")
+        out = _on_stream(foreign, stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=dev))
+    args, cache = _attention_args(q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len,
+                                  window, sinks, sm_scale, page_size, k_scale, v_scale,
+                                  k_scale_cache, v_scale_cache, out)
+    need = _attention_workspace(args, cache)
     ws = (None, 0)
     if need > 0:
         if workspace is None:
             workspace = _on_stream(foreign, stream,
                                    lambda: torch.empty(need, dtype=torch.uint8, device=dev))
-            made.append(workspace)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -173,6 +173,15 @@ struct RopeParams {
   int32_t pos64;
 };
 
+// A product rounded on its own.  The compiler would fuse it into the sum that
+// takes it (v_fma_mix_f32), which gives other last bits, and so now and then
+// another code, than the operator's definition.
+__device__ __forceinline__ float product(float a, float b) {
+  float x = a * b;
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 enum RopeKind { kNoRope = 0, kHalves = 1, kInterleaved = 2 };
 
 // Heads of a token are numbered q, then k, then v.  A lane's partner chunk
@@ -241,8 +250,8 @@ __global__ __launch_bounds__(kWave * kRowsWaves) void kvstore_rope_kernel(const 
         widen8<kFp16>(other[j], o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = __fmul_rn(x[i], cs[i]), b = __fmul_rn(o[i], sn[i]);
-          x[i] = d < half ? __fsub_rn(a, b) : __fadd_rn(a, b);
+          const float a = product(x[i], cs[i]), b = product(o[i], sn[i]);
+          x[i] = d < half ? a - b : a + b;
         }
         changed = true;
       }
@@ -252,8 +261,8 @@ __global__ __launch_bounds__(kWave * kRowsWaves) void kvstore_rope_kernel(const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
+          x[2 * i] = product(a, cs[i]) - product(b, sn[i]);
+          x[2 * i + 1] = product(b, cs[i]) + product(a, sn[i]);
         }
         changed = true;
       }
