@@ -216,6 +216,52 @@ __device__ __forceinline__ u32x2 read_column4(uint8_t* at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
 }
 
+// Loads from addresses that went through LDS: as global memory, not generic.
+template <typename T>
+__device__ __forceinline__ T load_global(uint64_t at) {
+  return *reinterpret_cast<__attribute__((address_space(1))) const T*>(at);
+}
+
+// Non-finite 16-bit values of a pair replaced by zeros, or kept alone.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool* special) {
+  constexpr uint32_t e = kFp16 ? 0x7C00u : 0x7F80u;
+  const bool lo = (w & e) == e, hi = (w & (e << 16)) == e << 16;
+  *special = *special || lo || hi;
+  return w & ~((lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u));
+}
+template <bool kFp16>
+__device__ __forceinline__ u32x4 finite8(u32x4 w, bool* special) {
+  return u32x4{finite_pair<kFp16>(w.x, special), finite_pair<kFp16>(w.y, special),
+               finite_pair<kFp16>(w.z, special), finite_pair<kFp16>(w.w, special)};
+}
+
+// Element d of a cached V row, as a float; finite values give 0.  For the rare
+// rows that see a NaN or an infinity (see the kernels' "special" passes).
+template <int kFmt, bool kFp16>
+__device__ __forceinline__ float special_at(const Params& p, uint32_t head, int32_t page,
+                                            int32_t off, int32_t d) {
+  const uint8_t* row = p.v.data + (int64_t)page * p.v.page + (int64_t)off * p.v.offset +
+                       (int64_t)head * p.v.head;
+  const uint8_t* sc = p.v.scales + (int64_t)page * p.v.s_page + (int64_t)off * p.v.s_offset;
+  float x;
+  if constexpr (kFmt == kFmt16) {
+    const uint16_t w = reinterpret_cast<const uint16_t*>(row)[d];
+    x = kFp16 ? (float)__builtin_bit_cast(_Float16, w) : __uint_as_float((uint32_t)w << 16);
+  } else if constexpr (kFmt == kFmtFp4) {
+    x = sc[(int64_t)head * p.v.s_head + d / 32] == 255 ? __builtin_nanf("") : 0.0f;
+  } else {
+    const uint32_t w = row[d];
+    const float y = kFmt == kFmtE4M3 ? __builtin_amdgcn_cvt_f32_fp8((int)w, 0)
+                                     : __builtin_amdgcn_cvt_f32_bf8((int)w, 0);
+    x = p.scale_kind == KVATTN_TENSOR
+            ? y
+            : y * *reinterpret_cast<const float*>(
+                      sc + (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * p.v.s_head : 0));
+  }
+  return __builtin_isfinite(x) ? 0.0f : x;
+}
+
 // Page and offset of a key.
 __device__ __forceinline__ void key_page(const Params& p, int32_t key, int32_t* page,
                                          int32_t* off) {
@@ -231,6 +277,22 @@ __device__ __forceinline__ void key_page(const Params& p, int32_t key, int32_t* 
 // What a row of new tokens sees.
 __device__ __forceinline__ bool sees(const Params& p, int32_t pos, int32_t key) {
   return key <= pos && (pos - key < p.window || key < p.sinks);
+}
+
+// Bits 0 ... n - 1 (none below 1, all from 64 on).
+__device__ __forceinline__ unsigned long long low_bits(int32_t n) {
+  const unsigned long long some = (1ull << (n & 63)) - 1ull;
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : some;
+}
+
+// sees() for the keys key0 + j of a step, as bits j: those that are there, at
+// most pos, and inside the window or among the first tokens.
+__device__ __forceinline__ unsigned long long seen_bits(const Params& p, int32_t pos, int32_t key0,
+                                                        unsigned long long ok) {
+  const int32_t last = pos - key0;   // >= -2^31 + 1: positions are above -2^31 / 2
+  const unsigned long long behind = last < p.window ? 0ull : low_bits(last - p.window + 1);
+  return ok & low_bits(last < 64 ? last + 1 : 64) &
+         (~behind | low_bits(p.sinks < key0 ? 0 : p.sinks - key0));
 }
 
 // A row of a tile: its token (row of q), q head, and index among all rows.

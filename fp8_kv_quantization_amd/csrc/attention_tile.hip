@@ -49,8 +49,8 @@ template <int kDim>
 struct Lds {
   alignas(16) uint8_t k[2][kStep * Shape<kDim>::kStrideK];
   alignas(16) uint8_t v[2][kStep * Shape<kDim>::kStrideV];
-  const uint8_t* at[kRing][2][kStep];  // K and V rows
-  const uint8_t* scale_at[kFmt == kFmtFp4 ? kRing : 1][2][kFmt == kFmtFp4 ? kStep : 1];
+  uint64_t at[kRing][2][kStep];        // addresses of K and V rows
+  uint64_t scale_at[kFmt == kFmtFp4 ? kRing : 1][2][kFmt == kFmtFp4 ? kStep : 1];
   alignas(16) float scale[kFp8 ? kRing : 1][2][kFp8 ? kStep : 4];
   unsigned long long ok[kRing];        // keys that are there
 };
@@ -136,10 +136,12 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     const int r = (step - s_begin) & (kRing - 1);
     // Slot 0 stands in for keys that are not there: its row is loaded and not used.
     const int64_t pg = there ? page : 0, of = there ? off : 0;
-    lds.at[r][w][lane] = side.data + pg * side.page + of * side.offset + (int64_t)head * side.head;
+    lds.at[r][w][lane] = reinterpret_cast<uint64_t>(side.data) + pg * side.page + of * side.offset +
+                         (int64_t)head * side.head;
     const int64_t sc_at = pg * side.s_page + of * side.s_offset;
     if constexpr (kFmt == kFmtFp4)
-      lds.scale_at[r][w][lane] = side.scales + sc_at + (int64_t)head * side.s_head;
+      lds.scale_at[r][w][lane] =
+          reinterpret_cast<uint64_t>(side.scales) + sc_at + (int64_t)head * side.s_head;
     if constexpr (kFp8) {
       float sc = 1.0f;
       if (dyn && there)
@@ -165,31 +167,54 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int row = (row0 & (kStep - 1)) + i * S::kRows;
-      kr[i] = *reinterpret_cast<const u32x4*>(lds.at[r][0][row] + from);
-      vr[i] = *reinterpret_cast<const u32x4*>(lds.at[r][1][row] + from);
+      kr[i] = load_global<u32x4>(lds.at[r][0][row] + from);
+      vr[i] = load_global<u32x4>(lds.at[r][1][row] + from);
       if constexpr (kFmt == kFmtFp4) {
-        kb[i] = lds.scale_at[r][0][row][writes ? col / 32 : 0];
-        vb[i] = lds.scale_at[r][1][row][writes ? col / 32 : 0];
+        kb[i] = load_global<uint8_t>(lds.scale_at[r][0][row] + (writes ? col / 32 : 0));
+        vb[i] = load_global<uint8_t>(lds.scale_at[r][1][row] + (writes ? col / 32 : 0));
       }
     }
   };
-  auto put = [&](uint8_t* dst, u32x4 x, uint32_t byte, float sc) {
+  // Some row of the tile does not see some key of the step.
+  auto mixed_step = [&](int32_t step, unsigned long long ok) {
+    const int32_t key0 = t.key_of(step);
+    return ok != ~0ull || key0 + kStep - 1 > t.p_lo ||
+           !(t.p_hi - key0 < p.window || key0 + kStep - 1 < p.sinks);
+  };
+  // Where rows see different keys, NaN and infinities of V (0 * V is not 0 for
+  // them) are left out of the product, and added at the end to the rows that do
+  // see them.
+  const bool ragged = t.p_lo != t.p_hi;
+  bool special = false;
+  auto put = [&](uint8_t* dst, u32x4 x, uint32_t byte, float sc, bool clean) {
     if constexpr (kFmt == kFmt16) {
+      if (clean) x = finite8<kFp16>(x, &special);
       *reinterpret_cast<u32x4*>(dst) = x;
     } else if constexpr (kFmt == kFmtFp4) {
+      if (clean && byte == 255) {
+        special = true;
+        byte = 127;
+        x = u32x4{0u, 0u, 0u, 0u};
+      }
       const float s4 = __uint_as_float(byte << 23);
       const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<u32x4*>(dst + 16 * i) = values8<kFp16, kFmt>(e[i], 0, s4);
     } else {
-      *reinterpret_cast<u32x4*>(dst) = values8<kFp16, kFmt>(x.x, x.y, sc);
-      *reinterpret_cast<u32x4*>(dst + 16) = values8<kFp16, kFmt>(x.z, x.w, sc);
+      u32x4 a = values8<kFp16, kFmt>(x.x, x.y, sc), b = values8<kFp16, kFmt>(x.z, x.w, sc);
+      if (clean) {
+        a = finite8<kFp16>(a, &special);
+        b = finite8<kFp16>(b, &special);
+      }
+      *reinterpret_cast<u32x4*>(dst) = a;
+      *reinterpret_cast<u32x4*>(dst + 16) = b;
     }
   };
   auto store_rows = [&](int32_t step) {
     const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
     const unsigned long long ok = lds.ok[r];
+    const bool clean = ragged && mixed_step(step, ok);
     if (ok != ~0ull) {   // 0 * V must be 0 for keys that are not there
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i) {
@@ -202,10 +227,10 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int row = row0 + i * S::kRows;
-      put(lds.k[b] + row * S::kStrideK + 2 * col, kr[i], kb[i], 1.0f);
+      put(lds.k[b] + row * S::kStrideK + 2 * col, kr[i], kb[i], 1.0f, false);
       // V's power of two goes into the values, exactly; its significand into the weights
       put(lds.v[b] + row * S::kStrideV + 2 * col, vr[i], vb[i],
-          kFp8 ? lds.scale[kFp8 ? r : 0][1][kFp8 ? row : 0] : 1.0f);
+          kFp8 ? lds.scale[kFp8 ? r : 0][1][kFp8 ? row : 0] : 1.0f, clean);
     }
   };
 
@@ -229,7 +254,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 
   for (int32_t step = s_begin; step < s_end; ++step) {
     const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
-    const int32_t key0 = t.key_of(step);
+    int32_t key0 = t.key_of(step);
     const bool more = step + 1 < s_end;
     if (more) load_rows(step + 1);
     place(step + 2, page_next);
@@ -249,8 +274,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 
     // Key of value i of half h: key0 + 32 h + 8 (i / 4) + 4 half + i % 4.
     const unsigned long long ok = lds.ok[r];
-    const bool mixed = ok != ~0ull || key0 + kStep - 1 > t.p_lo ||
-                       !(t.p_hi - key0 < p.window || key0 + kStep - 1 < p.sinks);
+    const bool mixed = mixed_step(step, ok);
     float vm[kFp8 ? 32 : 1];
     if constexpr (kFp8) {
       if (dyn) {
@@ -270,25 +294,16 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
           }
       }
     }
-    uint32_t seen = ~0u;
+    uint32_t seen[2] = {~0u, ~0u};   // bit 8 (i / 4) + i % 4 of half h: the row sees value i
     if (mixed) {
-      // sees() of key key0 + 4 half + j, with the differences taken once (and
-      // kept inside the loop: the compiler would carry 32 of them across it)
-      int32_t last = pos - key0 - 4 * (int)half;                       // j <= last
-      int32_t first = last < p.window ? -1 : last - p.window;          // j > first
-      int32_t sink = min(p.sinks - key0, kStep) - 4 * (int)half;       // or j < sink
-      uint32_t ok0 = (uint32_t)(ok >> (4 * half)), ok1 = (uint32_t)((ok >> 32) >> (4 * half));
-      asm volatile("" : "+v"(last), "+v"(first), "+v"(sink), "+v"(ok0), "+v"(ok1));
-      seen = 0;
+      const unsigned long long bits = seen_bits(p, pos, key0, ok) >> (4 * half);
+      seen[0] = (uint32_t)bits;
+      seen[1] = (uint32_t)(bits >> 32);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int32_t jj = 8 * (i >> 2) + (i & 3), j = 32 * h + jj;
-          const bool see = ((h ? ok1 : ok0) >> jj & 1u) != 0 && j <= last && (j > first || j < sink);
-          s[h][i] = see ? s[h][i] : kNegInf;
-          seen |= see ? 1u << (16 * h + i) : 0u;
-        }
+        for (int i = 0; i < 16; ++i)
+          s[h][i] = seen[h] & (1u << (8 * (i >> 2) + (i & 3))) ? s[h][i] : kNegInf;
     }
     float top = kNegInf;
 #pragma unroll
@@ -320,7 +335,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            s[h][i] = (seen >> (16 * h + i)) & 1u ? s[h][i] * vm[16 * h + i] : 0.0f;
+            s[h][i] = seen[h] & (1u << (8 * (i >> 2) + (i & 3))) ? s[h][i] * vm[16 * h + i] : 0.0f;
       }
     }
     u32x4 pt[4];   // P^T operands of 16 keys each
@@ -339,61 +354,40 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
       const u32x2 y = read_column4(vp + (16 * k + 8) * S::kStrideV + dt * 64);
       return u32x4{x.x, x.y, y.x, y.y};
     };
-    bool apart = false;
-    if (mixed && t.p_lo != t.p_hi) {
-      // 0 * V is not 0 where V holds a NaN or an infinity, which must not reach
-      // the rows that do not see it.
-      f32x16 z;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-#pragma unroll 1
-      for (int k = 0; k < 4 * kDt; ++k)
-        z = mfma32<kFp16>(v_operand(k & 3, k >> 2), u32x4{0u, 0u, 0u, 0u}, z);
-      float zz = 0.0f;
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) zz += z[i];
-      apart = __ballot(!(zz == 0.0f)) != 0;
-    }
-    if (!apart) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int dt = 0; dt < kDt; ++dt)
-          acc[dt] = mfma32<kFp16>(v_operand(k, dt), pt[k], acc[dt]);
-    } else {
-      // One key at a time, added to the rows that see it.
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll 1
-        for (int j = 0; j < 16; ++j) {
-          const int e = (j & 3) + 4 * (j >> 3);   // element of the operand, in lanes of half (j >> 2) & 1
-          const bool mine = (int)half == ((j >> 2) & 1);
-          const uint32_t keep = mine ? ((e & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-          const uint32_t k0 = e < 2 ? keep : 0u, k1 = (e >> 1) == 1 ? keep : 0u;
-          const uint32_t k2 = (e >> 1) == 2 ? keep : 0u, k3 = e > 5 ? keep : 0u;
-          const u32x4 only = u32x4{k0, k1, k2, k3};
-          const int32_t key = 16 * k + j;
-          const bool see = ((ok >> key) & 1ull) && sees(p, pos, key0 + key);
-          const u32x4 one = pt[k] & only;
-#pragma unroll
-          for (int dt = 0; dt < kDt; ++dt) {
-            f32x16 y;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-            y = mfma32<kFp16>(v_operand(k, dt) & only, one, y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[dt][i] += see ? y[i] : 0.0f;
-            __builtin_amdgcn_sched_barrier(0);   // one at a time: this is the rare path
-          }
-        }
-      }
-    }
+      for (int dt = 0; dt < kDt; ++dt) acc[dt] = mfma32<kFp16>(v_operand(k, dt), pt[k], acc[dt]);
 
     if (more) store_rows(step + 1);
     __syncthreads();
   }
   if (__ballot(met_bad) != 0 && tid == 0 && head == 0)
     report(p.flag, (uint32_t)(t.token0 + t.row0 / (int32_t)p.group));
+
+  if (__syncthreads_or(special)) {
+    // Rare: V's NaN and infinities of the steps that they were left out of, for
+    // the rows that see them.
+    for (int32_t step = s_begin; step < s_end; ++step) {
+      const int32_t key0 = t.key_of(step);
+      for (int32_t key = key0; key < min(key0 + kStep, t.end); ++key) {
+        if (key < t.low && key >= p.sinks) continue;
+        int32_t page, off;
+        key_page(p, key, &page, &off);
+        page = table[page];
+        if (page < 0 || page >= p.num_pages || !sees(p, pos, key)) continue;
+        int32_t d0 = 4 * half;
+        asm volatile("" : "+v"(d0));   // keeps 16 kDt comparisons from being carried along
+#pragma unroll
+        for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int32_t d = d0 + dt * 32 + 8 * (i >> 2) + (i & 3);
+            if (d < p.dim) acc[dt][i] += special_at<kFmt, kFp16>(p, head, page, off, d);
+          }
+      }
+    }
+  }
 
   l += __shfl_xor(l, 32);
   if (my_row >= t.rows) return;
