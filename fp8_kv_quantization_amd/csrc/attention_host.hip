@@ -42,7 +42,7 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   if (a.src_dtype != KVSTORE_SRC_BF16 && a.src_dtype != KVSTORE_SRC_FP16) return KVSTORE_ERR_DTYPE;
   if (c.num_heads <= 0 || c.head_dim <= 0 || c.head_dim > 256 || a.q_heads <= 0 ||
       a.q_heads % c.num_heads || c.page_size <= 0 || c.page_size > INT32_MAX || c.num_slots <= 0 ||
-      c.num_slots / c.page_size > INT32_MAX || a.max_pages == 0 ||
+      c.num_slots < c.page_size || c.num_slots / c.page_size > INT32_MAX || a.max_pages == 0 ||
       (int64_t)a.max_pages > INT32_MAX / c.page_size || a.max_len < 0 || a.window < 0 ||
       a.sinks < 0 || !(a.sm_scale >= 0.0f) || !(a.sm_scale <= 3.4e38f))
     return KVSTORE_ERR_SHAPE;
@@ -51,7 +51,8 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t group = a.q_heads / c.num_heads;
   const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q == 0 || a.max_q > a.tokens ? a.tokens : a.max_q;
   const int64_t rows = max_q * group;
-  plan->nr = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+  // 64 rows of more than 128 dims do not fit a wave's registers
+  plan->nr = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 && c.head_dim <= 128 ? 4 : 0;
   const int64_t step = plan->nr > 0 ? kvattn::kSplitStep : kvattn::kTileStep;
   plan->padded_dim = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   const int64_t tile = plan->nr > 0 ? 16 * plan->nr : kvattn::kTileRows;

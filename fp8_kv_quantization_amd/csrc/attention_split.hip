@@ -30,8 +30,14 @@ namespace {
 constexpr int kWaves = 4;
 constexpr bool kFp16 = KVATTN_FP16 != 0;
 constexpr int kFmt = KVATTN_FMT;
+constexpr bool kFp8 = kFmt == kFmtE4M3 || kFmt == kFmtE5M2;
 constexpr float kLazy = 8.0f;
 constexpr int kStep = kSplitStep;
+
+// Bytes that d elements take.
+__device__ __forceinline__ uint32_t bytes_of(int32_t d) {
+  return kFmt == kFmt16 ? 2 * d : kFmt == kFmtFp4 ? d / 2 : d;
+}
 
 template <int kDim>
 struct Shape {
@@ -47,12 +53,23 @@ struct Shape {
   static constexpr int kStrideO = kDim + 4;             // floats of an O row in LDS
 };
 
+// A lane's piece of a K row: 16 bytes, or 8 of a 4-bit row of up to 64 dims.
+template <int kBytes>
+__device__ __forceinline__ void load_piece(uint64_t at, u32x4* x) {
+  if constexpr (kBytes == 16) {
+    *x = load_global<u32x4>(at);
+  } else {
+    const u32x2 y = load_global<u32x2>(at);
+    *x = u32x4{y.x, y.y, 0u, 0u};
+  }
+}
+
 template <int kDim>
 struct WaveLds {
   alignas(16) uint8_t v[kStep * Shape<kDim>::kStrideV];
-  int64_t at[2][kStep];      // K and V offsets of the step's keys, -1: not loaded
-  int64_t scale_at[2][kFmt == kFmtFp4 ? kStep : 1];
-  alignas(16) float scale[2][kFmt == kFmtE4M3 || kFmt == kFmtE5M2 ? kStep : 4];
+  uint64_t at[2][kStep];     // addresses of the step's K and V rows, where they are kept
+  uint64_t scale_at[2][kFmt == kFmtFp4 ? kStep : 1];
+  alignas(16) float scale[2][kFp8 ? kStep : 4];
 };
 
 __device__ __forceinline__ float group_max4(float x) {   // over the 4 lanes l, l^16, l^32, l^48
@@ -60,7 +77,16 @@ __device__ __forceinline__ float group_max4(float x) {   // over the 4 lanes l, 
   return fmaxf(x, __shfl_xor(x, 32));
 }
 
-template <int kDim, int kNr>
+__device__ __forceinline__ uint32_t load_scalar(const int32_t* p) {
+  return *reinterpret_cast<__attribute__((address_space(4))) const uint32_t*>(
+      reinterpret_cast<uint64_t>(p));
+}
+
+// kWholePages: page_size is a multiple of 16, so that the 16 keys of a half step
+// lie in one page: their rows have a scalar base and fixed lane offsets, and
+// page table reads are scalar loads.  Otherwise lanes look their keys' pages up
+// and hand the addresses over through LDS.
+template <int kDim, int kNr, bool kWholePages>
 __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params p) {
   typedef Shape<kDim> S;
   constexpr int kTileRows = 16 * kNr;
@@ -70,7 +96,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   __shared__ float s_m[kWaves][kTileRows], s_l[kWaves][kTileRows];
 
   const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
-  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const uint32_t g = lane >> 4, c16 = lane & 15;
   Tile<kStep> t;
   if (!tile_of(p, slot, kTileRows, &t)) return;
@@ -81,10 +107,9 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   const int32_t s_end = min(t.steps, s_begin + chunk);
   WaveLds<kDim>& my = lds[w];
 
-  const bool dyn = (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) && p.scale_kind != KVATTN_TENSOR;
-  const bool tensor = (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) && p.scale_kind == KVATTN_TENSOR;
+  const bool dyn = kFp8 && p.scale_kind != KVATTN_TENSOR;
   float c = p.scale2, v_scale = 1.0f;
-  if (tensor) {
+  if (kFp8 && !dyn) {
     if (p.k.scales) c *= *reinterpret_cast<const float*>(p.k.scales);
     if (p.v.scales) v_scale = *reinterpret_cast<const float*>(p.v.scales);
   }
@@ -119,123 +144,223 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   }
 
   const int32_t* table = p.table + (int64_t)t.seq * p.table_stride;
-  const int32_t kk = lane & 31;
-  // The page of this lane's key of a step (lanes l and l + 32 take key l): -2
-  // where no row of the tile sees the key.
-  auto page_id = [&](int32_t step) -> int32_t {
-    const int32_t key = t.key_of(step) + kk;
-    if (key >= t.end || (key < t.low && key >= p.sinks)) return -2;
+  const int64_t head_k = (int64_t)head * p.k.head, head_v = (int64_t)head * p.v.head;
+  bool met_bad = false;
+
+  // Keys of a step that some row of the tile may see, as bits.
+  auto wanted = [&](int32_t key0) -> uint32_t {
+    const uint32_t in = (uint32_t)low_bits(t.end - key0);
+    return in & (~(uint32_t)low_bits(t.low - key0) | (uint32_t)low_bits(p.sinks < key0 ? 0 : p.sinks - key0));
+  };
+
+  // The pages of a step: of its halves (scalar), or of the lane's key lane & 31
+  // (-2: no row of the tile sees it).
+  struct Pages { int32_t a, b; };
+  auto pages_of = [&](int32_t step) -> Pages {
+    const int32_t key0 = t.key_of(step);
     int32_t page, off;
-    key_page(p, key, &page, &off);
-    return table[page];
+    if constexpr (kWholePages) {
+      const int32_t last = (t.end - 1) & ~15;   // a half without keys looks up the last one with some
+      const int32_t ka = min(key0, last), kb = min(key0 + 16, last);
+      key_page(p, ka, &page, &off);
+      const int32_t a = load_scalar(table + page);
+      key_page(p, kb, &page, &off);
+      return {a, (int32_t)load_scalar(table + page)};
+    } else {
+      const int32_t kk = lane & 31;
+      if (!((wanted(key0) >> kk) & 1u)) return {-2, -2};
+      key_page(p, key0 + kk, &page, &off);
+      return {table[page], 0};
+    }
   };
 
   u32x4 kr[2][S::kLoadsK], vr[S::kLoadsV];
   uint32_t kb[2][kFmt == kFmtFp4 ? S::kLoadsK : 1], vb[kFmt == kFmtFp4 ? S::kLoadsV : 1];
+  float sc = 1.0f;     // K's (lanes 0-31) or V's scale of key lane & 31
   uint32_t ok = 0;     // the step's keys that are there
-  bool met_bad = false;
+
+  // Lanes past the head's dims load a row's start, and write or multiply nothing.
+  const int32_t dk = g * 8 * S::kEB;
+  const int32_t v_row = lane / S::kLanesV, dv = (lane % S::kLanesV) * S::kVE;
+  const bool writes = dv < p.dim;
+  const uint32_t v_from = writes ? bytes_of(dv) : 0;
 
   // Places the step's keys and issues their loads.
-  auto load_step = [&](int32_t step, int32_t page) {
-    const int32_t key = t.key_of(step) + kk;
-    int32_t ignore, off;
-    key_page(p, key, &ignore, &off);
-    const bool there = page >= 0 && page < p.num_pages;
-    met_bad = met_bad || (page != -2 && !there);
-    const Side& side = lane < 32 ? p.k : p.v;
-    const int64_t at = (int64_t)page * side.page + (int64_t)off * side.offset + (int64_t)head * side.head;
-    my.at[lane >> 5][kk] = there ? at : -1;
-    if constexpr (kFmt == kFmtFp4)
-      my.scale_at[lane >> 5][kk] =
-          (int64_t)page * side.s_page + (int64_t)off * side.s_offset + (int64_t)head * side.s_head;
-    if constexpr (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) {
-      float sc = 1.0f;
-      if (dyn && there)
-        sc = *reinterpret_cast<const float*>(
-            side.scales + (int64_t)page * side.s_page + (int64_t)off * side.s_offset +
-            (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
-      my.scale[lane >> 5][kk] = sc;
-    }
-    ok = (uint32_t)__ballot(there);
-    __builtin_amdgcn_wave_barrier();
+  auto load_step = [&](int32_t step, Pages pg) {
+    const int32_t key0 = t.key_of(step);
+    const uint32_t want = wanted(key0);
+    if constexpr (kWholePages) {
+      const bool ga = (uint32_t)pg.a < (uint32_t)p.num_pages, gb = (uint32_t)pg.b < (uint32_t)p.num_pages;
+      const uint32_t there = (ga ? 0xFFFFu : 0u) | (gb ? 0xFFFF0000u : 0u);
+      met_bad = met_bad || (want & ~there) != 0;
+      ok = want & there;
+      // page 0 stands in for a page that is not there
+      const int64_t page[2] = {ga ? pg.a : 0, gb ? pg.b : 0};
+      int32_t ignore, off[2];
+      key_page(p, key0, &ignore, &off[0]);
+      key_page(p, key0 + 16, &ignore, &off[1]);
+      uint64_t kbase[2], vbase[2], ksbase[2], vsbase[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t a = my.at[0][h * 16 + c16];
-#pragma unroll
-      for (int i = 0; i < S::kLoadsK; ++i) {
-        const int d = i * 32 * S::kEB + g * 8 * S::kEB;
-        u32x4 x = u32x4{0u, 0u, 0u, 0u};
-        uint32_t b = 127;
-        if (a >= 0 && d < p.dim) {
-          if constexpr (kFmt == kFmt16) {
-            x = *reinterpret_cast<const u32x4*>(p.k.data + a + 2 * d);
-          } else if constexpr (kFmt == kFmtFp4) {
-            if constexpr (S::kEB == 4) {
-              x = *reinterpret_cast<const u32x4*>(p.k.data + a + d / 2);
-            } else {
-              const u32x2 y = *reinterpret_cast<const u32x2*>(p.k.data + a + d / 2);
-              x.x = y.x;
-              x.y = y.y;
-            }
-            b = p.k.scales[my.scale_at[0][h * 16 + c16] + d / 32];
-          } else {
-            x = *reinterpret_cast<const u32x4*>(p.k.data + a + d);
-          }
+      for (int h = 0; h < 2; ++h) {
+        kbase[h] = reinterpret_cast<uint64_t>(p.k.data) + page[h] * p.k.page + off[h] * p.k.offset + head_k;
+        vbase[h] = reinterpret_cast<uint64_t>(p.v.data) + page[h] * p.v.page + off[h] * p.v.offset + head_v;
+        ksbase[h] = reinterpret_cast<uint64_t>(p.k.scales) + page[h] * p.k.s_page + off[h] * p.k.s_offset;
+        vsbase[h] = reinterpret_cast<uint64_t>(p.v.scales) + page[h] * p.v.s_page + off[h] * p.v.s_offset;
+        if (kFmt == kFmtFp4 || p.scale_kind == KVATTN_TOKEN_HEAD) {
+          ksbase[h] += (int64_t)head * p.k.s_head;
+          vsbase[h] += (int64_t)head * p.v.s_head;
         }
-        kr[h][i] = x;
-        if constexpr (kFmt == kFmtFp4) kb[h][i] = b;
       }
-    }
 #pragma unroll
-    for (int i = 0; i < S::kLoadsV; ++i) {
-      const int row = i * S::kRowsV + lane / S::kLanesV;
-      const int d = (lane % S::kLanesV) * S::kVE;
-      const int64_t a = my.at[1][row];
-      u32x4 x = u32x4{0u, 0u, 0u, 0u};
-      uint32_t b = 127;
-      if (a >= 0 && d < p.dim) {
-        x = *reinterpret_cast<const u32x4*>(p.v.data + a + (kFmt == kFmt16 ? 2 * d : kFmt == kFmtFp4 ? d / 2 : d));
-        if constexpr (kFmt == kFmtFp4) b = p.v.scales[my.scale_at[1][row] + d / 32];
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::kLoadsK; ++i) {
+          const int32_t d = dk + i * 32 * S::kEB;
+          const uint32_t from = c16 * (uint32_t)p.k.offset + (d < p.dim ? bytes_of(d) : 0);
+          load_piece<kFmt == kFmtFp4 ? 4 * S::kEB : 16>(kbase[h] + from, &kr[h][i]);
+          if constexpr (kFmt == kFmtFp4)
+            kb[h][i] = load_global<uint8_t>(ksbase[h] + (uint32_t)(c16 * (uint32_t)p.k.s_offset + (d < p.dim ? d / 32 : 0)));
+        }
+#pragma unroll
+      for (int i = 0; i < S::kLoadsV; ++i) {
+        uint64_t base, sbase;
+        uint32_t row;
+        if constexpr (S::kRowsV > 16) {   // both halves in one access
+          base = lane < 32 ? vbase[0] : vbase[1];
+          sbase = lane < 32 ? vsbase[0] : vsbase[1];
+          row = v_row & 15;
+        } else {
+          constexpr int per = 16 / (S::kRowsV > 16 ? 16 : S::kRowsV);
+          base = vbase[i / per] + (i % per) * S::kRowsV * p.v.offset;
+          sbase = vsbase[i / per] + (i % per) * S::kRowsV * p.v.s_offset;
+          row = v_row;
+        }
+        vr[i] = load_global<u32x4>(base + (uint32_t)(row * (uint32_t)p.v.offset + v_from));
+        if constexpr (kFmt == kFmtFp4)
+          vb[i] = load_global<uint8_t>(sbase + (uint32_t)(row * (uint32_t)p.v.s_offset + (writes ? dv / 32 : 0)));
       }
-      vr[i] = x;
-      if constexpr (kFmt == kFmtFp4) vb[i] = b;
+      if constexpr (kFp8) {
+        if (dyn) {
+          const uint64_t base = lane < 32 ? (lane < 16 ? ksbase[0] : ksbase[1]) : (lane < 48 ? vsbase[0] : vsbase[1]);
+          sc = load_global<float>(base + (int64_t)c16 * (lane < 32 ? p.k.s_offset : p.v.s_offset));
+          if (!((ok >> (lane & 31)) & 1u)) sc = 1.0f;
+        }
+      }
+    } else {
+      const int32_t kk = lane & 31;
+      int32_t ignore, off;
+      key_page(p, key0 + kk, &ignore, &off);
+      const bool there = pg.a >= 0 && pg.a < p.num_pages;
+      met_bad = met_bad || (pg.a != -2 && !there);
+      ok = (uint32_t)__ballot(there);
+      // slot 0 stands in for keys that are not there
+      const int64_t page = there ? pg.a : 0, of = there ? off : 0;
+      const Side& side = lane < 32 ? p.k : p.v;
+      my.at[lane >> 5][kk] = reinterpret_cast<uint64_t>(side.data) + page * side.page + of * side.offset +
+                             (lane < 32 ? head_k : head_v);
+      const uint64_t scales = reinterpret_cast<uint64_t>(side.scales) + page * side.s_page + of * side.s_offset;
+      if constexpr (kFmt == kFmtFp4) my.scale_at[lane >> 5][kk] = scales + (int64_t)head * side.s_head;
+      if constexpr (kFp8) {
+        sc = 1.0f;
+        if (dyn && there)
+          sc = load_global<float>(scales + (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::kLoadsK; ++i) {
+          const int32_t d = dk + i * 32 * S::kEB;
+          load_piece<kFmt == kFmtFp4 ? 4 * S::kEB : 16>(
+              my.at[0][h * 16 + c16] + (d < p.dim ? bytes_of(d) : 0), &kr[h][i]);
+          if constexpr (kFmt == kFmtFp4)
+            kb[h][i] = load_global<uint8_t>(my.scale_at[0][h * 16 + c16] + (d < p.dim ? d / 32 : 0));
+        }
+#pragma unroll
+      for (int i = 0; i < S::kLoadsV; ++i) {
+        const int row = i * S::kRowsV + v_row;
+        vr[i] = load_global<u32x4>(my.at[1][row] + v_from);
+        if constexpr (kFmt == kFmtFp4) vb[i] = load_global<uint8_t>(my.scale_at[1][row] + (writes ? dv / 32 : 0));
+      }
+      __builtin_amdgcn_wave_barrier();
     }
+  };
+
+  // Where rows see different keys, NaN and infinities of V (0 * V is not 0 for
+  // them) are left out of the product, and added at the end to the rows that do
+  // see them.
+  const bool ragged = t.p_lo != t.p_hi;
+  bool special = false;
+  auto mixed_step = [&](int32_t key0) {   // some row does not see some key
+    return ok != 0xFFFFFFFFu || key0 + kStep - 1 > t.p_lo ||
+           !(t.p_hi - key0 < p.window || key0 + kStep - 1 < p.sinks);
   };
 
   // V of the step into LDS as 16-bit values.
-  auto store_v = [&]() {
+  auto store_v = [&](bool mixed) {
+    const bool clean = ragged && mixed;
 #pragma unroll
     for (int i = 0; i < S::kLoadsV; ++i) {
-      const int row = i * S::kRowsV + lane / S::kLanesV;
-      uint8_t* dst = my.v + row * S::kStrideV + (lane % S::kLanesV) * S::kVE * 2;
+      const int row = i * S::kRowsV + v_row;
+      u32x4 x = vr[i];
+      uint32_t byte = kFmt == kFmtFp4 ? vb[kFmt == kFmtFp4 ? i : 0] : 0;
+      if (mixed) {   // 0 * V must be 0 for keys that are not there
+        const bool there = (ok >> row) & 1u;
+        x = there ? x : u32x4{0u, 0u, 0u, 0u};
+        byte = there ? byte : 127u;
+      }
+      uint8_t* dst = my.v + row * S::kStrideV + 2 * dv;
       if constexpr (kFmt == kFmt16) {
-        *reinterpret_cast<u32x4*>(dst) = vr[i];
+        if (clean) x = finite8<kFp16>(x, &special);
+        if (writes) *reinterpret_cast<u32x4*>(dst) = x;
       } else if constexpr (kFmt == kFmtFp4) {
-        const float sc = __uint_as_float(vb[i] << 23);
-        const uint32_t x[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
+        if (clean && byte == 255) {
+          special = true;
+          byte = 127;
+          x = u32x4{0u, 0u, 0u, 0u};
+        }
+        const float s4 = __uint_as_float(byte << 23);
+        const uint32_t e4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<u32x4*>(dst + 16 * e) = values8<kFp16, kFmt>(x[e], 0, sc);
+          if (writes) *reinterpret_cast<u32x4*>(dst + 16 * e) = values8<kFp16, kFmt>(e4[e], 0, s4);
       } else {
         // The scale's power of two goes into the values, exactly; its
         // significand into the weights.
-        const float sc = my.scale[1][row];
-        *reinterpret_cast<u32x4*>(dst) = values8<kFp16, kFmt>(vr[i].x, vr[i].y, sc);
-        *reinterpret_cast<u32x4*>(dst + 16) = values8<kFp16, kFmt>(vr[i].z, vr[i].w, sc);
+        const float s8 = dyn ? my.scale[1][row] : 1.0f;
+        u32x4 y = values8<kFp16, kFmt>(x.x, x.y, s8), z = values8<kFp16, kFmt>(x.z, x.w, s8);
+        if (clean) {
+          y = finite8<kFp16>(y, &special);
+          z = finite8<kFp16>(z, &special);
+        }
+        if (writes) {
+          *reinterpret_cast<u32x4*>(dst) = y;
+          *reinterpret_cast<u32x4*>(dst + 16) = z;
+        }
       }
     }
   };
 
+  if (p.dim < kDim) {   // the columns that no lane writes
+    for (uint32_t i = lane; i < sizeof(my.v) / 16; i += 64)
+      reinterpret_cast<u32x4*>(my.v)[i] = u32x4{0u, 0u, 0u, 0u};
+  }
+
   int32_t step = s_begin + (int32_t)w;
-  int32_t page_next = -2;
+  Pages next = {-2, -2};
   if (step < s_end) {
-    load_step(step, page_id(step));
-    if (step + kWaves < s_end) page_next = page_id(step + kWaves);
+    load_step(step, pages_of(step));
+    next = pages_of(min(step + kWaves, s_end - 1));
   }
   for (; step < s_end; step += kWaves) {
     const int32_t key0 = t.key_of(step);
     const uint32_t ok_now = ok;
-    store_v();
+    const bool mixed = mixed_step(key0);
+    if constexpr (kFp8) {
+      if (dyn) my.scale[lane >> 5][lane & 31] = sc;
+      __builtin_amdgcn_wave_barrier();
+    }
+    store_v(mixed);
 
     // S^T, in 16-key halves.
     f32x4 s[2][kNr];
@@ -245,7 +370,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
       for (int n = 0; n < kNr; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks) {
-        const u32x4 raw = kr[h][ks / S::kEB];
+        u32x4 raw = kr[h][ks / S::kEB];
         constexpr int kEB = S::kEB;
         const int e = ks % kEB;
         u32x4 a;
@@ -257,6 +382,8 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         } else {
           a = e ? values8<kFp16, kFmt>(raw.z, raw.w, 1.0f) : values8<kFp16, kFmt>(raw.x, raw.y, 1.0f);
         }
+        // q is 0 past the head's dims; what was loaded in their place need not be finite
+        if (p.dim < kDim && dk + (ks / kEB) * 32 * kEB + e * 8 >= p.dim) a = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int n = 0; n < kNr; ++n) s[h][n] = mfma16<kFp16>(a, q[n][ks], s[h][n]);
       }
@@ -264,7 +391,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 
     // Scales of the lane's keys: 4g ... 4g + 3 of each half.
     f32x4 ksc[2], vsc[2];
-    if constexpr (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) {
+    if constexpr (kFp8) {
       if (dyn) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -279,34 +406,25 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 
     // The next step's loads fly during the rest of this one.
     if (step + kWaves < s_end) {
-      load_step(step + kWaves, page_next);
-      if (step + 2 * kWaves < s_end) page_next = page_id(step + 2 * kWaves);
+      load_step(step + kWaves, next);
+      next = pages_of(min(step + 2 * kWaves, s_end - 1));
     }
 
-    // Some row does not see some key of the step.
-    const bool mixed = ok_now != 0xFFFFFFFFu || key0 + kStep - 1 > t.p_lo ||
-                       !(t.p_hi - key0 < p.window || key0 + kStep - 1 < p.sinks);
-    uint32_t seen[kNr];   // bit 4 h + i: the row sees the lane's key i of half h
     u32x4 pt[kNr];        // P^T operand
 #pragma unroll
     for (int n = 0; n < kNr; ++n) {
       float x[8];
       float top = kNegInf;
-      seen[n] = 0xFFu;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           x[4 * h + i] = s[h][n][i] * (dyn ? c * ksc[h][i] : c);
+      uint32_t seen = ~0u;   // bits i and 16 + i: the row sees the lane's key i of half 0 and 1
       if (mixed) {
-        seen[n] = 0;
+        seen = (uint32_t)seen_bits(p, pos[n], key0, ok_now) >> (4 * g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t j = (i >> 2) * 16 + 4 * g + (i & 3);
-          const bool see = ((ok_now >> j) & 1u) && sees(p, pos[n], key0 + j);
-          x[i] = see ? x[i] : kNegInf;
-          seen[n] |= see ? 1u << i : 0u;
-        }
+        for (int i = 0; i < 8; ++i) x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? x[i] : kNegInf;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
@@ -330,7 +448,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float y = x[i] * vsc[i >> 2][i & 3];
-          x[i] = (seen[n] >> i) & 1u ? y : 0.0f;
+          x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? y : 0.0f;
         }
       }
       pt[n] = u32x4{pack_pair<kFp16>(x[0], x[1]), pack_pair<kFp16>(x[2], x[3]),
@@ -340,58 +458,44 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     // O^T += V^T P^T.
     __builtin_amdgcn_wave_barrier();
     uint8_t* const col = my.v + (4 * g + (c16 >> 2)) * S::kStrideV + (c16 & 3) * 8;
-    u32x4 vt[kDt];
 #pragma unroll
     for (int dt = 0; dt < kDt; ++dt) {
       const u32x2 a = read_column4(col + dt * 32);
       const u32x2 b = read_column4(col + 16 * S::kStrideV + dt * 32);
-      vt[dt] = u32x4{a.x, a.y, b.x, b.y};
-    }
-    bool apart = false;
-    if (mixed && t.p_lo != t.p_hi) {
-      // Rows see different keys.  0 * V is not 0 where V holds a NaN or an
-      // infinity, which must not reach the rows that do not see it.
-      f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
+      const u32x4 vt = u32x4{a.x, a.y, b.x, b.y};
 #pragma unroll
-      for (int dt = 0; dt < kDt; ++dt) z = mfma16<kFp16>(vt[dt], u32x4{0u, 0u, 0u, 0u}, z);
-      const float zz = z[0] + z[1] + z[2] + z[3];
-      apart = __ballot(!(zz == 0.0f)) != 0;
-    }
-    if (!apart) {
-#pragma unroll
-      for (int dt = 0; dt < kDt; ++dt)
-#pragma unroll
-        for (int n = 0; n < kNr; ++n) acc[dt][n] = mfma16<kFp16>(vt[dt], pt[n], acc[dt][n]);
-    } else {
-      // One key at a time, added to the rows that see it.
-      for (int j = 0; j < kStep; ++j) {
-        const int h = j >> 4, gj = (j >> 2) & 3, e = 4 * h + (j & 3);
-        const bool mine = (int)g == gj;
-        // the pair of the operand that holds the key, and the half of the pair
-        const uint32_t keep = mine ? ((e & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-#pragma unroll
-        for (int n = 0; n < kNr; ++n) {
-          const uint32_t in[4] = {pt[n].x, pt[n].y, pt[n].z, pt[n].w};
-          u32x4 one = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) one[k] = (e >> 1) == k ? in[k] & keep : 0u;
-          const bool see = ((ok_now >> j) & 1u) && sees(p, pos[n], key0 + j);
-#pragma unroll
-          for (int dt = 0; dt < kDt; ++dt) {
-            u32x4 va = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) va[k] = (e >> 1) == k ? vt[dt][k] & keep : 0u;
-            const f32x4 y = mfma16<kFp16>(va, one, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[dt][n][i] += see ? y[i] : 0.0f;
-          }
-        }
-      }
+      for (int n = 0; n < kNr; ++n) acc[dt][n] = mfma16<kFp16>(vt, pt[n], acc[dt][n]);
     }
     __builtin_amdgcn_wave_barrier();
   }
   if (__ballot(met_bad) != 0 && head == 0 && lane == 0)
     report(p.flag, (uint32_t)(t.token0 + t.row0 / (int32_t)p.group));
+
+  if (__ballot(special) != 0) {
+    // Rare: V's NaN and infinities of the steps that they were left out of, for
+    // the rows that see them.
+    for (step = s_begin + (int32_t)w; step < s_end; step += kWaves) {
+      const int32_t first = t.key_of(step);
+      for (int32_t key = first; key < min(first + kStep, t.end); ++key) {
+        if (key < t.low && key >= p.sinks) continue;
+        int32_t page, off;
+        key_page(p, key, &page, &off);
+        page = table[page];
+        if (page < 0 || page >= p.num_pages) continue;
+        int32_t d0 = 4 * g;
+        asm volatile("" : "+v"(d0));
+#pragma unroll
+        for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (d0 + dt * 16 + i >= p.dim) continue;
+            const float x = special_at<kFmt, kFp16>(p, head, page, off, d0 + dt * 16 + i);
+#pragma unroll
+            for (int n = 0; n < kNr; ++n) acc[dt][n][i] += sees(p, pos[n], key) ? x : 0.0f;
+          }
+      }
+    }
+  }
 
   // Join the waves.
 #pragma unroll
@@ -475,15 +579,26 @@ int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) 
              : KVSTORE_ERR_HIP;
 }
 
-template <int kNr>
+template <int kNr, bool kWholePages>
 int launch_nr(const Params& p, int padded_dim, hipStream_t stream) {
   const dim3 grid(p.tile_slots * p.kv_heads, (uint32_t)p.splits);
-  void (*kernel)(Params) = padded_dim == 64    ? kvattn_split_kernel<64, kNr>
-                           : padded_dim == 128 ? kvattn_split_kernel<128, kNr>
-                                               : kvattn_split_kernel<256, kNr>;
+  // (the host asks for 64 rows up to 128 dims only)
+  void (*kernel)(Params) = padded_dim == 64    ? kvattn_split_kernel<64, kNr, kWholePages>
+                           : padded_dim == 128 ? kvattn_split_kernel<128, kNr, kWholePages>
+                                               : kvattn_split_kernel<256, kNr < 4 ? kNr : 2, kWholePages>;
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
   return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads), p, stream);
+}
+
+template <int kNr>
+int launch_pages(const Params& p, int padded_dim, hipStream_t stream) {
+  // lane offsets into 16 rows are 32-bit
+  const int64_t most = INT32_MAX / 32;
+  const bool whole = p.page_size % 16 == 0 && p.k.offset <= most && p.v.offset <= most &&
+                     p.k.s_offset <= most && p.v.s_offset <= most;
+  return whole ? launch_nr<kNr, true>(p, padded_dim, stream)
+               : launch_nr<kNr, false>(p, padded_dim, stream);
 }
 
 }  // namespace
@@ -499,9 +614,9 @@ int launch_nr(const Params& p, int padded_dim, hipStream_t stream) {
 int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int nr,
                                         hipStream_t stream) {
   switch (nr) {
-    case 1: return launch_nr<1>(p, padded_dim, stream);
-    case 2: return launch_nr<2>(p, padded_dim, stream);
-    default: return launch_nr<4>(p, padded_dim, stream);
+    case 1: return launch_pages<1>(p, padded_dim, stream);
+    case 2: return launch_pages<2>(p, padded_dim, stream);
+    default: return launch_pages<4>(p, padded_dim, stream);
   }
 }
 
