@@ -105,6 +105,9 @@ EXPORTED = ("kvstore_copy", "kvstore_fp8_paged", "kvstore_fp8_paged_e5m2",
 if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+if not any(f.startswith("_kvstore_torch") and f.endswith(".so") for f in os.listdir(_HERE)):
+    raise ImportError("_kvstore_torch is not built; run "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`")
 
 # ---------------------------------------------------------------------------
 # C ABI, one to one: the same names and arguments as include/kvstore.h
@@ -371,132 +374,24 @@ def store_kv_fp8_paged_dynamic(k, v, k_cache, v_cache, cache_loc, k_scale_cache,
         raise KVStoreError(st, "kvstore_fp8_paged_dynamic")
 
 
-def _src_code(dtype, what) -> int:
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return SRC_BF16
-    if dtype == torch.float16:
-        return SRC_FP16
-    raise TypeError(f"{what} must be bfloat16 or float16, not {dtype}")
+_fast = None   # _kvstore_torch, once it is needed: it loads torch
 
 
-def _scalar(s, what):
-    """Data pointer of an optional one-element fp32 GPU tensor."""
-    if s is None:
-        return None
-    if s.dtype != _torch().float32 or s.numel() != 1 or not s.is_cuda:
-        raise TypeError(f"{what} must be one-element fp32 GPU tensors")
-    return s.data_ptr()
+def _tensor_calls():
+    global _fast
+    if _fast is None:
+        _torch()   # its libraries, which the binding is linked against
+        from . import _kvstore_torch
+        _fast = _kvstore_torch
+    return _fast
 
 
-def _block_scale_strides(sc, H, blocks, page_size):
-    """((page, offset, head) byte strides, slots) of a flat [slots, H, blocks]
-    or paged [pages, page_size, H, blocks] e8m0 scale cache."""
-    torch = _torch()
-    if sc.dtype not in (torch.uint8, torch.float8_e8m0fnu) or not sc.is_cuda:
-        raise TypeError("4-bit caches take uint8 or float8_e8m0fnu GPU scale caches")
-    if sc.shape[-2:] != (H, blocks) or (blocks > 1 and sc.stride(-1) != 1):
-        raise ValueError(f"a 4-bit scale cache ends in [H, D/32] = [{H}, {blocks}], contiguous")
-    if sc.dim() == 3:
-        return (sc.stride(0) * page_size, sc.stride(0), sc.stride(1)), sc.shape[0]
-    if sc.dim() == 4 and sc.shape[1] == page_size:
-        return sc.stride()[:3], sc.shape[0] * page_size
-    raise ValueError("a 4-bit scale cache is [slots, H, D/32] or [pages, page_size, H, D/32]")
-
-
-def _paged_cache(k_cache, v_cache, page_size, size_limit, src_dtype, k_scale, v_scale,
-                 k_scale_cache, v_scale_cache, reads):
-    """(members of kvstore_paged_cache, H, D, slots) of a K and a V cache.
-    `reads`: the call reads scales (a store into FP8 caches has none)."""
-    torch = _torch()
-    dt = k_cache.dtype
-    if dt != v_cache.dtype:
-        raise TypeError(f"k_cache and v_cache must share one dtype ({dt} != {v_cache.dtype})")
-    if page_size < 1:
-        raise ValueError("page_size must be positive")
-    shape = k_cache.shape
-    if v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    strides = []
-    es = k_cache.element_size()
-    for c in (k_cache, v_cache):
-        st = c.stride()
-        if st[-1] != 1:
-            raise ValueError("cache dim stride must be 1")
-        if len(st) == 3:
-            strides += (st[0] * page_size * es, st[0] * es, st[1] * es)
-        elif len(st) == 4:
-            strides += (st[0] * es, st[1] * es, st[2] * es)
-        else:
-            raise ValueError(f"a cache is 3-D (flat) or 4-D (paged), not {len(st)}-D")
-    H, D = shape[-2], shape[-1]
-    if len(shape) == 3:
-        slots = shape[0]
-        if slots % page_size:
-            raise ValueError(f"a flat cache of {slots} slots does not split into pages of {page_size}")
-    else:
-        slots = shape[0] * page_size
-        if shape[1] != page_size:
-            raise ValueError(f"the paged cache holds {shape[1]} slots per page, not page_size={page_size}")
-    kind, scales, scale_strides = SCALES_TENSOR, (None, None), (0, 0, 0, 0, 0, 0)
-    if dt == torch.float4_e2m1fn_x2:
-        fmt, kind, D = FMT_FP4, SCALES_BLOCK, 2 * D
-        if k_scale_cache is None or v_scale_cache is None:
-            raise ValueError("4-bit caches need k_scale_cache and v_scale_cache")
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("4-bit caches have block scales, not tensor scales")
-        if D % 32:
-            raise ValueError(f"a 4-bit head_dim is a multiple of 32, not {D}")
-        kss, kslots = _block_scale_strides(k_scale_cache, H, D // 32, page_size)
-        vss, vslots = _block_scale_strides(v_scale_cache, H, D // 32, page_size)
-        if kslots != slots or vslots != slots:
-            raise ValueError("scale caches must cover the same slots as the caches")
-        scales = (k_scale_cache.data_ptr(), v_scale_cache.data_ptr())
-        scale_strides = (*kss, *vss)
-    elif dt in (torch.bfloat16, torch.float16):
-        if dt != src_dtype:
-            raise TypeError(f"{dt} caches go with {dt} rows, not {src_dtype}")
-        if any(s is not None for s in (k_scale, v_scale, k_scale_cache, v_scale_cache)):
-            raise ValueError("16-bit caches have no scales")
-        fmt = FMT_BF16 if dt == torch.bfloat16 else FMT_FP16
-    elif dt in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2):
-        fmt = FMT_E5M2 if dt == torch.float8_e5m2 else FMT_E4M3FN
-        if (k_scale_cache is None) != (v_scale_cache is None):
-            raise ValueError("give both scale caches or neither")
-        if k_scale_cache is not None:
-            if not reads:
-                raise ValueError("a store into FP8 caches takes inverse scales, not scale caches")
-            if k_scale is not None or v_scale is not None:
-                raise ValueError("give scale caches or tensor scales, not both")
-            paged = k_scale_cache.dim() - (len(shape) == 4)
-            per_head = paged == 2
-            kind = SCALES_TOKEN_HEAD if per_head else SCALES_TOKEN
-            kss, kslots = _scale_strides(k_scale_cache, per_head, H, page_size)
-            vss, vslots = _scale_strides(v_scale_cache, per_head, H, page_size)
-            if kslots != slots or vslots != slots:
-                raise ValueError("scale caches must cover the same slots as the caches")
-            scales = (k_scale_cache.data_ptr(), v_scale_cache.data_ptr())
-            scale_strides = (*kss, *vss)
-        elif reads:
-            scales = (_scalar(k_scale, "scales"), _scalar(v_scale, "scales"))
-    else:
-        raise TypeError(f"a {dt} cache is none of the formats: the rows' 16-bit dtype, uint8 or "
-                        "float8_e4m3fn (e4m3fn codes), float8_e5m2, float4_e2m1fn_x2")
-    limit = _size_limit(size_limit, slots)
-    return (k_cache.data_ptr(), v_cache.data_ptr(), fmt, kind, H, D, page_size, limit, *strides,
-            *scales, *scale_strides), H, D, slots
-
-
-def _call(entry, dev, stream, *args) -> None:
-    """Calls a store entry on `dev` and its stream; raises on a bad status."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        st = entry(*args, _stream_handle(stream, dev))
-    else:
-        with torch.cuda.device(dev):
-            st = entry(*args, _stream_handle(stream, dev))
-    if st != OK:
-        raise KVStoreError(st, entry.__name__)
+def _under(stream, call):
+    """`call` with `stream` current (None: the stream that is)."""
+    if stream is None:
+        return call()
+    with _torch().cuda.stream(stream):
+        return call()
 
 
 def store_kv_rope_paged(k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q=None, q_out=None,
@@ -511,47 +406,15 @@ def store_kv_rope_paged(k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q
     (i, i + rot/2), or (2i, 2i + 1) if interleaved.  FP8 caches take inverse
     scales as in store_kv_fp8_paged, 4-bit caches scale caches.  cos_sin None
     (with positions None): no rotation."""
-    torch = _torch()
-    dev = _device_of(k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q, q_out, inv_k_scale,
-                     inv_v_scale, k_scale_cache, v_scale_cache)
-    src = _src_code(k.dtype, "k and v")
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("q, k and v must share one dtype")
-    cache, H, D, _ = _paged_cache(k_cache, v_cache, page_size, size_limit, k.dtype, None, None,
-                                  k_scale_cache, v_scale_cache, False)
-    if cache[2] not in (FMT_E4M3FN, FMT_E5M2) and not (inv_k_scale is None and inv_v_scale is None):
-        raise ValueError("only FP8 caches take inverse scales")
-    T = k.shape[0]
-    if v.shape[0] != T or cache_loc.dim() != 1 or cache_loc.shape[0] != T:
-        raise ValueError("cache_loc must be [T] with T = k.shape[0] = v.shape[0]")
-    ks, vs = _input_strides(k, H, D), _input_strides(v, H, D)
-    qp = qop = None
-    Hq, qs, qos = 0, (0, 0), (0, 0)
-    if q is not None:
-        q_out = q if q_out is None else q_out
-        if q.shape[0] != T or q_out.shape != q.shape or q_out.dtype != q.dtype:
-            raise ValueError("q and q_out must be [T, Hq, D] or [T, Hq*D] of one dtype")
-        Hq = q.shape[1] if q.dim() == 3 else q.shape[1] // D if q.dim() == 2 else 0
-        qs, qos = _input_strides(q, Hq, D), _input_strides(q_out, Hq, D)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if (positions is None) != (cos_sin is None):
-        raise ValueError("give positions and cos_sin, or neither")
-    rot, pos = 0, (None, IDX_I32, None, 0, 0)
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.stride(1) != 1:
-            raise TypeError("cos_sin must be fp32 [positions, rot] with contiguous rows")
-        if positions.dim() != 1 or positions.shape[0] != T or (T > 1 and positions.stride(0) != 1):
-            raise ValueError("positions must be a contiguous [T]")
-        rot = cos_sin.shape[1]
-        pos = (positions.data_ptr(), _idx_code(positions), cos_sin.data_ptr(),
-               cos_sin.stride(0) * 4, cos_sin.shape[0])
-    _call(kvstore_rope_paged, dev, stream,
-          (qp, qop, k.data_ptr(), v.data_ptr(), src, Hq, *qs, *qos, *ks, *vs), *pos, rot,
-          1 if interleaved else 0, cache_loc.data_ptr(), _idx_code(cache_loc),
-          cache_loc.stride(0) if T else 1, cache, _scalar(inv_k_scale, "inverse scales"),
-          _scalar(inv_v_scale, "inverse scales"), T)
+    if stream is not None:
+        return _under(stream, lambda: store_kv_rope_paged(
+            k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q, q_out, interleaved, page_size,
+            inv_k_scale, inv_v_scale, k_scale_cache, v_scale_cache, size_limit))
+    st = (_fast or _tensor_calls()).store_kv_rope_paged(
+        k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q, q_out, interleaved, page_size,
+        inv_k_scale, inv_v_scale, k_scale_cache, v_scale_cache, size_limit)
+    if st != OK:
+        raise KVStoreError(st, "kvstore_rope_paged")
 
 
 def store_kv_fp4_paged(k, v, k_cache, v_cache, cache_loc, k_scale_cache, v_scale_cache,
@@ -574,65 +437,15 @@ def load_kv_paged(k_cache, v_cache, cache_loc, k_out, v_out, page_size=16, k_sca
     the fp32 scale of the tensor (None: 1.0) or scale caches [slots(, H)] /
     [pages, page_size(, H)]; a row whose slot is out of range is left as it
     was and recorded."""
-    dev = _device_of(k_cache, v_cache, cache_loc, k_out, v_out, k_scale, v_scale, k_scale_cache,
-                     v_scale_cache)
-    dst = _src_code(k_out.dtype, "k_out and v_out")
-    if v_out.dtype != k_out.dtype:
-        raise TypeError("k_out and v_out must share one dtype")
-    cache, H, D, _ = _paged_cache(k_cache, v_cache, page_size, size_limit, k_out.dtype, k_scale,
-                                  v_scale, k_scale_cache, v_scale_cache, True)
-    T = k_out.shape[0]
-    if v_out.shape[0] != T or cache_loc.dim() != 1 or cache_loc.shape[0] != T:
-        raise ValueError("cache_loc must be [T] with T = k_out.shape[0] = v_out.shape[0]")
-    _call(kvstore_load_paged, dev, stream, cache, cache_loc.data_ptr(), _idx_code(cache_loc),
-          cache_loc.stride(0) if T else 1, k_out.data_ptr(), *_input_strides(k_out, H, D),
-          v_out.data_ptr(), *_input_strides(v_out, H, D), dst, T)
-
-
-def _attention_args(q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks,
-                    sm_scale, page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, out):
-    """Checks attention_paged's arguments; the members of
-    kvstore_attention_args up to the workspace, and those of the cache."""
-    torch = _torch()
-    src = _src_code(q.dtype, "q")
-    cache, H, D, _ = _paged_cache(k_cache, v_cache, page_size, None, q.dtype, k_scale, v_scale,
-                                  k_scale_cache, v_scale_cache, True)
-    if q.dim() != 3 or q.shape[2] != D or q.shape[1] % H:
-        raise ValueError(f"q must be [T, Hq, {D}] with Hq a multiple of {H}")
-    T, Hq = q.shape[0], q.shape[1]
-    if seq_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError("seq_lens must be [B] and page_table [B, pages]")
-    B = seq_lens.shape[0]
-    for t in (page_table, seq_lens, cu_q):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("page_table, seq_lens and cu_q must be int32")
-    if (B > 1 and seq_lens.stride(0) != 1) or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("seq_lens and the rows of page_table must be contiguous")
-    if cu_q is None:
-        if T != B:
-            raise ValueError(f"without cu_q every sequence has one token: {T} rows, {B} sequences")
-    elif cu_q.dim() != 1 or cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
-        raise ValueError("cu_q must be a contiguous [B + 1]")
-    if window < 0 or sinks < 0 or (max_q is not None and max_q < 0) or (
-            max_len is not None and max_len < 0):
-        raise ValueError("window, sinks, max_q and max_len must not be negative")
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
-        raise ValueError("out must have q's shape and dtype")
-    qs = q.stride()
-    os_ = (Hq * D, D, 1) if out is None else out.stride()
-    if qs[2] != 1 or os_[2] != 1:
-        raise ValueError("q and out must have a dim stride of 1")
-    return (q.data_ptr(), None if out is None else out.data_ptr(), qs[0] * 2, qs[1] * 2, os_[0] * 2,
-            os_[1] * 2, src, Hq, None if cu_q is None else cu_q.data_ptr(), T, B, min(max_q or 0, T),
-            page_table.data_ptr(), page_table.stride(0), page_table.shape[1], seq_lens.data_ptr(),
-            max_len or 0, window, sinks, D ** -0.5 if sm_scale is None else sm_scale), cache
-
-
-def _attention_workspace(args, cache) -> int:
-    need = kvstore_attention_workspace((*args, None, 0), cache)
-    if need < 0:
-        raise KVStoreError(need, "kvstore_attention_paged")
-    return need
+    if stream is not None:
+        return _under(stream, lambda: load_kv_paged(
+            k_cache, v_cache, cache_loc, k_out, v_out, page_size, k_scale, v_scale, k_scale_cache,
+            v_scale_cache, size_limit))
+    st = (_fast or _tensor_calls()).load_kv_paged(
+        k_cache, v_cache, cache_loc, k_out, v_out, page_size, k_scale, v_scale, k_scale_cache,
+        v_scale_cache, size_limit)
+    if st != OK:
+        raise KVStoreError(st, "kvstore_load_paged")
 
 
 def attention_paged_workspace(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=None,
@@ -640,9 +453,12 @@ def attention_paged_workspace(q, k_cache, v_cache, page_table, seq_lens, cu_q=No
                               v_scale=None, k_scale_cache=None, v_scale_cache=None) -> int:
     """Bytes of workspace that attention_paged needs for these arguments (by
     their shapes; 0: none)."""
-    return _attention_workspace(*_attention_args(
+    need = (_fast or _tensor_calls()).attention_paged(
         q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks, None,
-        page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, None))
+        page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, None, None, True)
+    if need < 0:
+        raise KVStoreError(need, "kvstore_attention_paged")
+    return need
 
 
 def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=None, max_len=None,
@@ -660,35 +476,16 @@ def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=
     attention_paged_workspace gives, in use until the call's work is done, so
     calls (or captured graphs) that may overlap need one each; by default the
     call takes one from torch's allocator."""
-    torch = _torch()
-    dev = _device_of(q, k_cache, v_cache, page_table, seq_lens, cu_q, k_scale, v_scale,
-                     k_scale_cache, v_scale_cache, out, workspace)
-    foreign = stream is not None and stream != torch.cuda.current_stream(dev)
-    if out is None:
-        out = _on_stream(foreign, stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=dev))
-    args, cache = _attention_args(q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len,
-                                  window, sinks, sm_scale, page_size, k_scale, v_scale,
-                                  k_scale_cache, v_scale_cache, out)
-    need = _attention_workspace(args, cache)
-    ws = (None, 0)
-    if need > 0:
-        if workspace is None:
-            workspace = _on_stream(foreign, stream,
-                                   lambda: torch.empty(need, dtype=torch.uint8, device=dev))
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call(kvstore_attention_paged, dev, stream, (*args, *ws), cache)
-    return out
-
-
-def _on_stream(foreign, stream, make):
-    """Allocates under `stream` where that is not the current one, so that the
-    allocator orders the memory's reuse by the stream that uses it."""
-    if not foreign:
-        return make()
-    with _torch().cuda.stream(stream):
-        return make()
+    if stream is not None:
+        return _under(stream, lambda: attention_paged(
+            q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks, sm_scale,
+            page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, out, workspace))
+    got = (_fast or _tensor_calls()).attention_paged(
+        q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks, sm_scale,
+        page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, out, workspace, False)
+    if type(got) is int:
+        raise KVStoreError(got, "kvstore_attention_paged")
+    return got
 
 
 def take_error(out, stream=None):

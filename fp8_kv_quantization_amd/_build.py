@@ -1,6 +1,7 @@
 """Builds libkvstore.so in-tree with hipcc for gfx950 (its objects are compiled
-side by side), and its CPython binding (_kvstore_py, gcc, linked against
-libkvstore.so)."""
+side by side), its CPython binding (_kvstore_py, gcc) and the tensor-level
+binding of the paged operators (_kvstore_torch, g++ against torch's headers),
+both linked against libkvstore.so."""
 from __future__ import annotations
 
 import os
@@ -18,6 +19,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 PY_SRC = os.path.join(PKG, "csrc", "kvstore_py.c")
 PY_EXT = os.path.join(PKG, "_kvstore_py" + sysconfig.get_config_var("EXT_SUFFIX"))
+TORCH_SRC = os.path.join(PKG, "csrc", "kvstore_torch.cpp")
+TORCH_EXT = os.path.join(PKG, "_kvstore_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",
@@ -58,6 +61,18 @@ def binding_command(out: str = PY_EXT) -> list:
             PY_SRC, "-L", PKG, "-lkvstore", "-Wl,-rpath,$ORIGIN", "-o", out]
 
 
+def torch_binding_command(out: str = TORCH_EXT) -> list:
+    import importlib.util
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-fvisibility=hidden",
+            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+            "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(ROCM, "include"), TORCH_SRC, "-L", PKG, "-lkvstore", "-L", lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN", "-o", out]
+
+
 def _run(cmd, out, what, verbose):
     tmp = out + ".tmp"
     cmd = [tmp if c == out else c for c in cmd]
@@ -71,8 +86,8 @@ def _run(cmd, out, what, verbose):
 
 
 def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
-    """Compile the HIP library and, for the in-tree library, the CPython
-    binding (always).  Writes atomically."""
+    """Compile the HIP library and, for the in-tree library, the two bindings
+    (always).  Writes atomically."""
     with tempfile.TemporaryDirectory() as tmp:
         made = [(src, os.path.join(tmp, name), [*flags, *extra]) for src, flags, name in objects()]
         with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
@@ -80,4 +95,5 @@ def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
         _run(link_command([m[1] for m in made], out), out, "hipcc (link)", verbose)
     if out == LIB:
         _run(binding_command(), PY_EXT, "gcc (binding)", verbose)
+        _run(torch_binding_command(), TORCH_EXT, "g++ (tensor binding)", verbose)
     return out

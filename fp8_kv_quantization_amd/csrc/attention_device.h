@@ -41,10 +41,6 @@ __device__ __forceinline__ int32_t clamp_row(const Params& p, int32_t r) {
 // and leave it room for all its tiles (floor(x + y) >= floor(x) + ceil(y) - 1),
 // so a block finds its sequence from cu_q alone, with no prefix sums; slots
 // beyond a sequence's tiles hold nothing.
-__device__ __forceinline__ int64_t slot_start(const Params& p, uint32_t b, uint32_t rows) {
-  return (int64_t)clamp_row(p, p.cu_q[b]) * p.group / rows + b;
-}
-
 // A tile: `rows` (token, head in group) pairs of one sequence, and its keys as
 // steps of kStep: first those of the first tokens, then those of the window.
 template <int kStep>
@@ -82,7 +78,7 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_
 template <int kStep>
 __device__ __forceinline__ bool tile_of(const Params& p, uint32_t slot, int32_t tile_rows,
                                         Tile<kStep>* t) {
-  int32_t begin, n;
+  int32_t begin, n, len;
   int32_t index;   // of the tile in its sequence
   if (p.cu_q == nullptr) {
     const uint32_t per = (p.group + tile_rows - 1) / tile_rows;
@@ -90,29 +86,36 @@ __device__ __forceinline__ bool tile_of(const Params& p, uint32_t slot, int32_t 
     index = slot - t->seq * per;
     begin = t->seq;
     n = 1;
+    len = uniform(p.seq_lens[t->seq]);
   } else {
     // The last sequence whose start is at most `slot`, by 64-way search: starts
     // increase, so the lanes that hold one at most `slot` are the first ones.
+    // The last round, over neighbours, has what the tile needs in its lanes.
     const uint32_t lane = threadIdx.x & 63;
     uint32_t lo = 0, size = p.seqs;
-    while (size > 0) {
+    for (;;) {
       const uint32_t stride = (size + 63) / 64;
-      const uint32_t b = lo + lane * stride;
-      const bool at_most = lane * stride < size && slot_start(p, b, tile_rows) <= slot;
-      const uint32_t k = __popcll(__ballot(at_most));
+      const uint32_t at = lane * stride, b = lo + (at < size ? at : size - 1);
+      const int32_t c0 = clamp_row(p, p.cu_q[b]), c1 = clamp_row(p, p.cu_q[b + 1]);
+      const int32_t keys = p.seq_lens[b];
+      const int64_t start = (int64_t)c0 * p.group / tile_rows + b;
+      const uint32_t k = __popcll(__ballot(at < size && start <= slot));
       if (k == 0) return false;   // before the first sequence
+      if (stride == 1) {
+        t->seq = uniform(lo + k - 1);
+        begin = __builtin_amdgcn_readlane(c0, k - 1);
+        n = __builtin_amdgcn_readlane(c1, k - 1) - begin;
+        len = __builtin_amdgcn_readlane(keys, k - 1);
+        const int64_t i = (int64_t)slot - ((int64_t)begin * p.group / tile_rows + t->seq);
+        if (n <= 0 || i * tile_rows >= (int64_t)n * p.group) return false;
+        index = (int32_t)i;
+        break;
+      }
       lo = uniform(lo + (k - 1) * stride);
       const uint32_t rest = size - (k - 1) * stride;
-      size = stride == 1 ? 0 : (rest < stride ? rest : stride);
+      size = uniform(rest < stride ? rest : stride);
     }
-    t->seq = lo;
-    begin = uniform(clamp_row(p, p.cu_q[lo]));
-    n = uniform(clamp_row(p, p.cu_q[lo + 1])) - begin;
-    const int64_t i = (int64_t)slot - slot_start(p, lo, tile_rows);
-    if (n <= 0 || i * tile_rows >= (int64_t)n * p.group) return false;
-    index = (int32_t)i;
   }
-  int32_t len = uniform(p.seq_lens[t->seq]);
   len = len < 0 ? 0 : len > p.max_keys ? p.max_keys : len;
   const int64_t all = (int64_t)n * p.group;
   const int64_t r0 = (int64_t)index * tile_rows;
@@ -312,37 +315,55 @@ __device__ __forceinline__ Row row_of(const Params& p, const Tile<kStep>& t, uin
   return x;
 }
 
-// Joins the splits of each row: 16 threads per row.
+// Joins the splits of each row: a wave per row, kJoinRows rows a block.  All of
+// a row's partial sums are loaded before any is needed.
+constexpr int kJoinRows = 4;
 template <bool kFp16, int kStep>
 __device__ __forceinline__ void join_splits(const Params& p, int32_t tile_rows, float v_scale) {
-  const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
+  const uint32_t parts = tile_rows / kJoinRows;
+  const uint32_t part = blockIdx.x % parts, turn = blockIdx.x / parts;
+  const uint32_t head = turn % p.kv_heads, slot = turn / p.kv_heads;
   Tile<kStep> t;
   if (!tile_of(p, slot, tile_rows, &t)) return;
   int32_t n_splits;
   split_steps(p, t, &n_splits);
-  if (n_splits == 1) return;
-  for (int r = threadIdx.x >> 4; r < t.rows; r += 16) {
-    const Row x = row_of(p, t, head, r);
-    const int64_t at = x.index * p.splits;
-    float top = kNegInf, sum = 0.0f;
-    for (int i = 0; i < n_splits; ++i) top = fmaxf(top, p.ws_ml[2 * (at + i)]);
-    for (int i = 0; i < n_splits; ++i) {
-      const float mi = p.ws_ml[2 * (at + i)];
-      if (mi != kNegInf) sum += p.ws_ml[2 * (at + i) + 1] * __builtin_amdgcn_exp2f(mi - top);
-    }
-    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-    for (int d = (threadIdx.x & 15) * 4; d < p.dim; d += 64) {
-      f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < n_splits; ++i) {
-        const float mi = p.ws_ml[2 * (at + i)];
-        if (mi == kNegInf) continue;
-        y += *reinterpret_cast<const f32x4*>(p.ws_o + (at + i) * p.dim + d) *
-             __builtin_amdgcn_exp2f(mi - top);
-      }
-      *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
-          u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
+  const int32_t r = part * kJoinRows + uniform(threadIdx.x >> 6);
+  if (n_splits == 1 || r >= t.rows) return;
+  const Row x = row_of(p, t, head, r);
+  const int64_t at = x.index * p.splits;
+  const int32_t lane = threadIdx.x & 63;
+  // lanes: four dims of a split each, as many splits side by side as fit
+  const int32_t quads = p.dim / 4, side = 64 / quads;
+  const int32_t d = lane % quads * 4, first = lane / quads;
+  float top = kNegInf;
+  for (int32_t i = lane; i < n_splits; i += 64) top = fmaxf(top, p.ws_ml[2 * (at + i)]);
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+  float sum = 0.0f;
+  f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (first < side) {
+#pragma unroll 4
+    for (int32_t i = first; i < n_splits; i += side) {
+      const float mi = p.ws_ml[2 * (at + i)], li = p.ws_ml[2 * (at + i) + 1];
+      const f32x4 o = *reinterpret_cast<const f32x4*>(p.ws_o + (at + i) * p.dim + d);
+      const float f = mi == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
+      sum += li * f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] += mi == kNegInf ? 0.0f : o[j] * f;
     }
   }
+  const float own_sum = sum;
+  const f32x4 own = y;
+  for (int32_t k = 1; k < side; ++k) {   // the other splits' lanes, in order
+    const int32_t from = lane % quads + k * quads;
+    sum += __shfl(own_sum, from);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] += __shfl(own[j], from);
+  }
+  if (first > 0) return;
+  const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+  *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
+      u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
 }
 
 }  // namespace kvattn

@@ -30,10 +30,12 @@ struct AttentionPlan {
   int64_t workspace;    // bytes
 };
 
-// Blocks to aim for: four for each of 256 CUs.
-constexpr int64_t kAttnBlocks = 1024;
+// Blocks to aim for (of 256 CUs' worth at a time, three or two a CU).
+constexpr int64_t kAttnSplitBlocks = 4096;
+constexpr int64_t kAttnTileBlocks = 256;
 // Fewest steps of a split: two for each of its four waves.
 constexpr int64_t kAttnMinChunk = 8;
+constexpr int64_t kAttnMostBlocks = (int64_t(1) << 24) - 1;
 constexpr int64_t kAttnMaxWorkspace = int64_t(1) << 30;
 
 int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c,
@@ -58,7 +60,9 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t tile = plan->nr > 0 ? 16 * plan->nr : kvattn::kTileRows;
   const int64_t slots = a.cu_q == nullptr ? a.seqs * ceil_div(group, tile)
                                           : (int64_t)a.tokens * group / tile + a.seqs;
-  if (slots * c.num_heads > (int64_t(1) << 24)) return KVSTORE_ERR_SHAPE;   // 2^32 work-items
+  // blocks of 256 threads: a launch stays below 2^32 work-items (with its splits:
+  // below)
+  if ((slots + 7) * c.num_heads > kAttnMostBlocks) return KVSTORE_ERR_SHAPE;
   plan->tile_slots = (uint32_t)slots;
   plan->max_keys = (int32_t)(a.max_pages * c.page_size);
   // Steps of a tile, at most (a longer sequence than max_len gets longer splits).
@@ -72,12 +76,17 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t tiles = a.cu_q == nullptr ? slots
                         : rows <= tile    ? (int64_t)a.seqs
                                           : (int64_t)a.tokens * group / tile + a.seqs / 2;
-  int64_t splits = ceil_div(kAttnBlocks, (tiles > 0 ? tiles : 1) * c.num_heads);
+  int64_t splits = ceil_div(plan->nr > 0 ? kAttnSplitBlocks : kAttnTileBlocks,
+                            (tiles > 0 ? tiles : 1) * c.num_heads);
   if (splits > steps / kAttnMinChunk) splits = steps / kAttnMinChunk;
   const int64_t row_bytes = (int64_t)a.tokens * a.q_heads * (c.head_dim + 2) * 4;
   if (row_bytes > 0 && splits > kAttnMaxWorkspace / row_bytes) splits = kAttnMaxWorkspace / row_bytes;
-  if (splits < 1) splits = 1;
+  const int64_t room = (kAttnMostBlocks / c.num_heads - 7) / (slots > 0 ? slots : 1);
+  if (splits > room) splits = room;
+  // the kernel that joins splits has a block for every four rows
+  if (slots * c.num_heads > kAttnMostBlocks / (tile / 4)) splits = 1;
   if (splits > 256) splits = 256;
+  if (splits < 1) splits = 1;
   plan->chunk_steps = (int32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
   splits = ceil_div(steps, plan->chunk_steps);
   plan->splits = (int32_t)(splits < 1 ? 1 : splits);

@@ -64,12 +64,13 @@ __device__ __forceinline__ void load_piece(uint64_t at, u32x4* x) {
   }
 }
 
-template <int kDim>
+template <int kDim, bool kWholePages>
 struct WaveLds {
   alignas(16) uint8_t v[kStep * Shape<kDim>::kStrideV];
-  uint64_t at[2][kStep];     // addresses of the step's K and V rows, where they are kept
-  uint64_t scale_at[2][kFmt == kFmtFp4 ? kStep : 1];
   alignas(16) float scale[2][kFp8 ? kStep : 4];
+  // addresses of the step's K and V rows
+  uint64_t at[2][kWholePages ? 1 : kStep];
+  uint64_t scale_at[2][kFmt == kFmtFp4 && !kWholePages ? kStep : 1];
 };
 
 __device__ __forceinline__ float group_max4(float x) {   // over the 4 lanes l, l^16, l^32, l^48
@@ -85,27 +86,38 @@ __device__ __forceinline__ uint32_t load_scalar(const int32_t* p) {
 // kWholePages: page_size is a multiple of 16, so that the 16 keys of a half step
 // lie in one page: their rows have a scalar base and fixed lane offsets, and
 // page table reads are scalar loads.  Otherwise lanes look their keys' pages up
-// and hand the addresses over through LDS.
-template <int kDim, int kNr, bool kWholePages>
-__global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params p) {
+// and hand the addresses over through LDS.  kFull: the head has kDim dims.
+template <int kDim, int kNr, bool kWholePages, bool kFull>
+__global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void kvattn_split_kernel(
+    const Params p) {
   typedef Shape<kDim> S;
   constexpr int kTileRows = 16 * kNr;
   constexpr int kKs = kDim / 32;     // k steps of Q K^T
   constexpr int kDt = kDim / 16;     // column tiles of O
-  __shared__ WaveLds<kDim> lds[kWaves];
+  __shared__ WaveLds<kDim, kWholePages> lds[kWaves];
   __shared__ float s_m[kWaves][kTileRows], s_l[kWaves][kTileRows];
 
-  const uint32_t head = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads;
+  // Blocks go to the eight XCDs in turn.  The heads of one tile and split take
+  // eight block numbers apart, so one XCD, which read the same cache lines where
+  // a head's row is shorter than one (and the scales of all heads).
+  const uint32_t turn = blockIdx.x >> 3, head = turn % p.kv_heads;
+  // A tile's splits go to different XCDs, and one split's number to all of them
+  // over the tiles: long sequences have more splits than others.
+  const uint32_t eight = turn / p.kv_heads;
+  const uint32_t unit = eight * 8 + ((blockIdx.x + eight + (eight >> 3)) & 7);
+  const uint32_t slot = unit / p.splits, split = unit - slot * p.splits;
+  if (slot >= p.tile_slots) return;
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const uint32_t g = lane >> 4, c16 = lane & 15;
   Tile<kStep> t;
   if (!tile_of(p, slot, kTileRows, &t)) return;
   int32_t n_splits;
   const int32_t chunk = split_steps(p, t, &n_splits);
-  if ((int32_t)blockIdx.y >= n_splits) return;
-  const int32_t s_begin = blockIdx.y * chunk;
+  if ((int32_t)split >= n_splits) return;
+  const int32_t s_begin = split * chunk;
   const int32_t s_end = min(t.steps, s_begin + chunk);
-  WaveLds<kDim>& my = lds[w];
+  WaveLds<kDim, kWholePages>& my = lds[w];
+  const int32_t dim = kFull ? kDim : p.dim;
 
   const bool dyn = kFp8 && p.scale_kind != KVATTN_TENSOR;
   float c = p.scale2, v_scale = 1.0f;
@@ -129,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     for (int ks = 0; ks < kKs; ++ks) {
       const int d = (ks / S::kEB) * 32 * S::kEB + g * 8 * S::kEB + (ks % S::kEB) * 8;
       q[n][ks] = u32x4{0u, 0u, 0u, 0u};
-      if (d < p.dim) q[n][ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
+      if (d < dim) q[n][ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
     }
   }
 
@@ -145,6 +157,11 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 
   const int32_t* table = p.table + (int64_t)t.seq * p.table_stride;
   const int64_t head_k = (int64_t)head * p.k.head, head_v = (int64_t)head * p.v.head;
+  const uint64_t k_from = reinterpret_cast<uint64_t>(p.k.data) + head_k;
+  const uint64_t v_from_head = reinterpret_cast<uint64_t>(p.v.data) + head_v;
+  const bool head_scales = kFmt == kFmtFp4 || p.scale_kind == KVATTN_TOKEN_HEAD;
+  const uint64_t ks_from = reinterpret_cast<uint64_t>(p.k.scales) + (head_scales ? (int64_t)head * p.k.s_head : 0);
+  const uint64_t vs_from = reinterpret_cast<uint64_t>(p.v.scales) + (head_scales ? (int64_t)head * p.v.s_head : 0);
   bool met_bad = false;
 
   // Keys of a step that some row of the tile may see, as bits.
@@ -182,7 +199,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
   // Lanes past the head's dims load a row's start, and write or multiply nothing.
   const int32_t dk = g * 8 * S::kEB;
   const int32_t v_row = lane / S::kLanesV, dv = (lane % S::kLanesV) * S::kVE;
-  const bool writes = dv < p.dim;
+  const bool writes = dv < dim;
   const uint32_t v_from = writes ? bytes_of(dv) : 0;
 
   // Places the step's keys and issues their loads.
@@ -195,20 +212,22 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
       met_bad = met_bad || (want & ~there) != 0;
       ok = want & there;
       // page 0 stands in for a page that is not there
-      const int64_t page[2] = {ga ? pg.a : 0, gb ? pg.b : 0};
+      const uint32_t page[2] = {ga ? (uint32_t)pg.a : 0u, gb ? (uint32_t)pg.b : 0u};
       int32_t ignore, off[2];
       key_page(p, key0, &ignore, &off[0]);
       key_page(p, key0 + 16, &ignore, &off[1]);
+      // strides are below 2^32 here (the launch sees to it)
       uint64_t kbase[2], vbase[2], ksbase[2], vsbase[2];
+      auto base_of = [&](uint64_t from, int64_t page_stride, int64_t stride, int h) {
+        return from + (uint64_t)page[h] * (uint32_t)page_stride + (uint64_t)(uint32_t)off[h] * (uint32_t)stride;
+      };
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        kbase[h] = reinterpret_cast<uint64_t>(p.k.data) + page[h] * p.k.page + off[h] * p.k.offset + head_k;
-        vbase[h] = reinterpret_cast<uint64_t>(p.v.data) + page[h] * p.v.page + off[h] * p.v.offset + head_v;
-        ksbase[h] = reinterpret_cast<uint64_t>(p.k.scales) + page[h] * p.k.s_page + off[h] * p.k.s_offset;
-        vsbase[h] = reinterpret_cast<uint64_t>(p.v.scales) + page[h] * p.v.s_page + off[h] * p.v.s_offset;
-        if (kFmt == kFmtFp4 || p.scale_kind == KVATTN_TOKEN_HEAD) {
-          ksbase[h] += (int64_t)head * p.k.s_head;
-          vsbase[h] += (int64_t)head * p.v.s_head;
+        kbase[h] = base_of(k_from, p.k.page, p.k.offset, h);
+        vbase[h] = base_of(v_from_head, p.v.page, p.v.offset, h);
+        if (kFmt == kFmtFp4 || dyn) {
+          ksbase[h] = base_of(ks_from, p.k.s_page, p.k.s_offset, h);
+          vsbase[h] = base_of(vs_from, p.v.s_page, p.v.s_offset, h);
         }
       }
 #pragma unroll
@@ -216,10 +235,10 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
 #pragma unroll
         for (int i = 0; i < S::kLoadsK; ++i) {
           const int32_t d = dk + i * 32 * S::kEB;
-          const uint32_t from = c16 * (uint32_t)p.k.offset + (d < p.dim ? bytes_of(d) : 0);
+          const uint32_t from = c16 * (uint32_t)p.k.offset + (d < dim ? bytes_of(d) : 0);
           load_piece<kFmt == kFmtFp4 ? 4 * S::kEB : 16>(kbase[h] + from, &kr[h][i]);
           if constexpr (kFmt == kFmtFp4)
-            kb[h][i] = load_global<uint8_t>(ksbase[h] + (uint32_t)(c16 * (uint32_t)p.k.s_offset + (d < p.dim ? d / 32 : 0)));
+            kb[h][i] = load_global<uint8_t>(ksbase[h] + (uint32_t)(c16 * (uint32_t)p.k.s_offset + (d < dim ? d / 32 : 0)));
         }
 #pragma unroll
       for (int i = 0; i < S::kLoadsV; ++i) {
@@ -272,9 +291,9 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         for (int i = 0; i < S::kLoadsK; ++i) {
           const int32_t d = dk + i * 32 * S::kEB;
           load_piece<kFmt == kFmtFp4 ? 4 * S::kEB : 16>(
-              my.at[0][h * 16 + c16] + (d < p.dim ? bytes_of(d) : 0), &kr[h][i]);
+              my.at[0][h * 16 + c16] + (d < dim ? bytes_of(d) : 0), &kr[h][i]);
           if constexpr (kFmt == kFmtFp4)
-            kb[h][i] = load_global<uint8_t>(my.scale_at[0][h * 16 + c16] + (d < p.dim ? d / 32 : 0));
+            kb[h][i] = load_global<uint8_t>(my.scale_at[0][h * 16 + c16] + (d < dim ? d / 32 : 0));
         }
 #pragma unroll
       for (int i = 0; i < S::kLoadsV; ++i) {
@@ -341,7 +360,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     }
   };
 
-  if (p.dim < kDim) {   // the columns that no lane writes
+  if (!kFull) {   // the columns that no lane writes
     for (uint32_t i = lane; i < sizeof(my.v) / 16; i += 64)
       reinterpret_cast<u32x4*>(my.v)[i] = u32x4{0u, 0u, 0u, 0u};
   }
@@ -365,12 +384,14 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
     // S^T, in 16-key halves.
     f32x4 s[2][kNr];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int n = 0; n < kNr; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        u32x4 raw = kr[h][ks / S::kEB];
+    for (int ks = 0; ks < kKs; ++ks) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 raw = kr[h][ks / S::kEB];
         constexpr int kEB = S::kEB;
         const int e = ks % kEB;
         u32x4 a;
@@ -383,7 +404,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
           a = e ? values8<kFp16, kFmt>(raw.z, raw.w, 1.0f) : values8<kFp16, kFmt>(raw.x, raw.y, 1.0f);
         }
         // q is 0 past the head's dims; what was loaded in their place need not be finite
-        if (p.dim < kDim && dk + (ks / kEB) * 32 * kEB + e * 8 >= p.dim) a = u32x4{0u, 0u, 0u, 0u};
+        if (!kFull && dk + (ks / kEB) * 32 * kEB + e * 8 >= dim) a = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int n = 0; n < kNr; ++n) s[h][n] = mfma16<kFp16>(a, q[n][ks], s[h][n]);
       }
@@ -488,7 +509,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (d0 + dt * 16 + i >= p.dim) continue;
+            if (d0 + dt * 16 + i >= dim) continue;
             const float x = special_at<kFmt, kFp16>(p, head, page, off, d0 + dt * 16 + i);
 #pragma unroll
             for (int n = 0; n < kNr; ++n) acc[dt][n][i] += sees(p, pos[n], key) ? x : 0.0f;
@@ -537,7 +558,7 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         row_l += mi == kNegInf ? 0.0f : s_l[i][n * 16 + r] * __builtin_amdgcn_exp2f(mi - row_top);
       }
       const Row x = row_of(p, t, head, n * 16 + r);
-      const int64_t at = x.index * p.splits + blockIdx.y;
+      const int64_t at = x.index * p.splits + split;
       const float inv = row_l == 0.0f ? 0.0f : v_scale / row_l;
 #pragma unroll
       for (int d = part * 4; d < kDim; d += 64) {
@@ -546,12 +567,12 @@ __global__ __launch_bounds__(64 * kWaves) void kvattn_split_kernel(const Params 
         for (int i = 0; i < kWaves; ++i)
           y += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[i].v) +
                                                r * S::kStrideO + d);
-        if (d >= p.dim) continue;
+        if (d >= dim) continue;
         if (n_splits == 1) {
           *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
               u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
         } else {
-          *reinterpret_cast<f32x4*>(p.ws_o + at * p.dim + d) = y;
+          *reinterpret_cast<f32x4*>(p.ws_o + at * dim + d) = y;
         }
       }
       if (n_splits > 1 && part == 0) {
@@ -579,26 +600,29 @@ int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) 
              : KVSTORE_ERR_HIP;
 }
 
-template <int kNr, bool kWholePages>
+template <int kNr, bool kWholePages, bool kFull>
 int launch_nr(const Params& p, int padded_dim, hipStream_t stream) {
-  const dim3 grid(p.tile_slots * p.kv_heads, (uint32_t)p.splits);
-  // (the host asks for 64 rows up to 128 dims only)
-  void (*kernel)(Params) = padded_dim == 64    ? kvattn_split_kernel<64, kNr, kWholePages>
-                           : padded_dim == 128 ? kvattn_split_kernel<128, kNr, kWholePages>
-                                               : kvattn_split_kernel<256, kNr < 4 ? kNr : 2, kWholePages>;
+  const dim3 grid((p.tile_slots * p.splits + 7) / 8 * 8 * p.kv_heads);
+  void (*kernel)(Params) = padded_dim == 64 ? kvattn_split_kernel<64, kNr, kWholePages, kFull>
+                                            : kvattn_split_kernel<128, kNr, kWholePages, kFull>;
+  if constexpr (kNr < 4)   // the host asks for 64 rows up to 128 dims only
+    if (padded_dim == 256) kernel = kvattn_split_kernel<256, kNr, kWholePages, kFull>;
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
-  return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads), p, stream);
+  return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads * (16 * kNr / kJoinRows)), p,
+             stream);
 }
 
 template <int kNr>
 int launch_pages(const Params& p, int padded_dim, hipStream_t stream) {
-  // lane offsets into 16 rows are 32-bit
+  // Whole pages: 32-bit strides, and 32-bit offsets of lanes into 16 rows.
   const int64_t most = INT32_MAX / 32;
   const bool whole = p.page_size % 16 == 0 && p.k.offset <= most && p.v.offset <= most &&
-                     p.k.s_offset <= most && p.v.s_offset <= most;
-  return whole ? launch_nr<kNr, true>(p, padded_dim, stream)
-               : launch_nr<kNr, false>(p, padded_dim, stream);
+                     p.k.s_offset <= most && p.v.s_offset <= most && p.k.page <= INT32_MAX &&
+                     p.v.page <= INT32_MAX && p.k.s_page <= INT32_MAX && p.v.s_page <= INT32_MAX;
+  if (!whole) return launch_nr<kNr, false, false>(p, padded_dim, stream);
+  return p.dim == padded_dim ? launch_nr<kNr, true, true>(p, padded_dim, stream)
+                             : launch_nr<kNr, true, false>(p, padded_dim, stream);
 }
 
 }  // namespace

@@ -445,7 +445,8 @@ int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int, hi
                                                : kvattn_tile_kernel<256>;
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
-  return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads), p, stream);
+  return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads * (kTileRows / kJoinRows)), p,
+             stream);
 }
 
 }  // namespace kvattn
