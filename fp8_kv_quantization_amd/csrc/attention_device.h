@@ -225,6 +225,14 @@ __device__ __forceinline__ T load_global(uint64_t at) {
   return *reinterpret_cast<__attribute__((address_space(1))) const T*>(at);
 }
 
+// 16 bytes a lane from global memory to LDS, at the wave's place plus 16 times
+// the lane (counted by vmcnt).
+__device__ __forceinline__ void load_to_lds(uint64_t from, uint8_t* wave_place) {
+  __builtin_amdgcn_global_load_lds(
+      reinterpret_cast<__attribute__((address_space(1))) void*>(from),
+      (__attribute__((address_space(3))) void*)wave_place, 16, 0, 0);
+}
+
 // Non-finite 16-bit values of a pair replaced by zeros, or kept alone.
 template <bool kFp16>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool* special) {

@@ -35,32 +35,44 @@ constexpr float kLazy = 8.0f;
 constexpr int kStep = kTileStep;
 constexpr int kRing = 4;   // steps whose row addresses are kept
 
-template <int kDim>
+// 16-bit rows of kDim dims are loaded straight into LDS (kDirect), with no
+// registers in between.  Such loads fill LDS in the order of the lanes, so rows
+// cannot be padded; instead the 16-byte pieces of a row change places with the
+// row's number, which keeps the reads of neighbouring rows on different banks.
+template <int kDim, bool kDirect>
 struct Shape {
   static constexpr int kElems = kFmt == kFmt16 ? 8 : kFmt == kFmtFp4 ? 32 : 16;   // of 16 bytes
   static constexpr int kLanes = kDim / kElems;                 // threads per row
   static constexpr int kRows = kThreads / kLanes;              // rows per access of the block
   static constexpr int kLoads = kRows >= kStep ? 1 : kStep / kRows;
-  static constexpr int kStrideK = 2 * kDim + 16;               // bytes of a row in LDS
-  static constexpr int kStrideV = 2 * kDim + 32;
+  static constexpr int kStrideK = 2 * kDim + (kDirect ? 0 : 16);   // bytes of a row in LDS
+  static constexpr int kStrideV = 2 * kDim + (kDirect ? 0 : 32);
+  static constexpr int kPieces = kDim / 8;                     // of 16 bytes, of a row
+  // Place of a K row's piece, and of a V row's (whose pairs stay together: a
+  // transposing read takes 32 bytes of each of four rows).
+  static constexpr uint32_t place_k(uint32_t row) { return kDirect ? row & (kPieces < 16 ? kPieces - 1 : 15) : 0; }
+  static constexpr uint32_t place_v(uint32_t row) { return kDirect ? 2 * (row & (kPieces < 16 ? 3 : 7)) : 0; }
 };
 
-template <int kDim>
+template <int kDim, bool kDirect>
 struct Lds {
-  alignas(16) uint8_t k[2][kStep * Shape<kDim>::kStrideK];
-  alignas(16) uint8_t v[2][kStep * Shape<kDim>::kStrideV];
+  alignas(256) uint8_t k[2][kStep * Shape<kDim, kDirect>::kStrideK];
+  alignas(256) uint8_t v[2][kStep * Shape<kDim, kDirect>::kStrideV];
   uint64_t at[kRing][2][kStep];        // addresses of K and V rows
   uint64_t scale_at[kFmt == kFmtFp4 ? kRing : 1][2][kFmt == kFmtFp4 ? kStep : 1];
   alignas(16) float scale[kFp8 ? kRing : 1][2][kFp8 ? kStep : 4];
+  alignas(16) float v_sig[kFp8 ? kRing : 1][kFp8 ? kStep : 4];   // significands of V's
   unsigned long long ok[kRing];        // keys that are there
 };
 
-template <int kDim>
+template <int kDim, bool kFull>
 __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_kernel(const Params p) {
-  typedef Shape<kDim> S;
+  constexpr bool kDirect = kFull && kFmt == kFmt16;
+  typedef Shape<kDim, kDirect> S;
+  const int32_t dim = kFull ? kDim : p.dim;
   constexpr int kKs = kDim / 16;    // k steps of Q K^T
   constexpr int kDt = kDim / 32;    // column tiles of O
-  __shared__ Lds<kDim> lds;
+  __shared__ Lds<kDim, kDirect> lds;
 
   const uint32_t head = blockIdx.x % p.kv_heads;
   // later tiles of a sequence see more keys: they start first
@@ -101,7 +113,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     for (int ks = 0; ks < kKs; ++ks) {
       const int d = ks * 16 + half * 8;
       q[ks] = u32x4{0u, 0u, 0u, 0u};
-      if (d < p.dim) q[ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
+      if (d < dim) q[ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
       q[ks] ^= flip;
     }
   }
@@ -125,6 +137,18 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     key_page(p, key, &page, &off);
     return table[page];
   };
+  // A step's scales are loaded by place and written to LDS a step later, so that
+  // no step waits for them.
+  float scale_late = 1.0f;
+  auto put_scales = [&](int32_t step, float scale) {
+    if constexpr (kFp8) {
+      if (w > 1 || step >= s_end) return;
+      const int r = (step - s_begin) & (kRing - 1);
+      lds.scale[r][w][lane] = scale;
+      if (is_v)
+        lds.v_sig[r][lane] = __uint_as_float((__float_as_uint(scale) & 0x807FFFFFu) | 0x3F800000u);
+    }
+  };
   auto place = [&](int32_t step, int32_t page) {
     if (w > 1 || step >= s_end) return;
     const int32_t key = t.key_of(step) + (int32_t)lane;
@@ -143,12 +167,11 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
       lds.scale_at[r][w][lane] =
           reinterpret_cast<uint64_t>(side.scales) + sc_at + (int64_t)head * side.s_head;
     if constexpr (kFp8) {
-      float sc = 1.0f;
+      scale_late = 1.0f;
       if (dyn && there)
-        sc = *reinterpret_cast<const float*>(
-            side.scales + sc_at +
+        scale_late = load_global<float>(
+            reinterpret_cast<uint64_t>(side.scales) + sc_at +
             (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
-      lds.scale[r][w][lane] = sc;
     }
     const unsigned long long ok = __ballot(there);
     if (tid == 0) lds.ok[r] = ok;
@@ -160,13 +183,21 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
   // Threads past the step's rows or the head's dims load a row's start and
   // write nothing.
   const int32_t row0 = tid / S::kLanes, col = (tid % S::kLanes) * S::kElems;
-  const bool writes = col < p.dim && row0 < kStep;
+  const bool writes = col < dim && row0 < kStep;
   const int32_t from = writes ? (kFmt == kFmt16 ? 2 * col : kFmt == kFmtFp4 ? col / 2 : col) : 0;
   auto load_rows = [&](int32_t step) {
     const int r = (step - s_begin) & (kRing - 1);
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int row = (row0 & (kStep - 1)) + i * S::kRows;
+      if constexpr (kDirect) {
+        const int b = (step - s_begin) & 1;
+        const uint32_t piece = tid % S::kLanes;
+        const int to = (i * S::kRows + w * (S::kRows / kWaves)) * S::kStrideK;   // of the wave
+        load_to_lds(lds.at[r][0][row] + 16 * (piece ^ S::place_k(row)), lds.k[b] + to);
+        load_to_lds(lds.at[r][1][row] + 16 * (piece ^ S::place_v(row)), lds.v[b] + to);
+        continue;
+      }
       kr[i] = load_global<u32x4>(lds.at[r][0][row] + from);
       vr[i] = load_global<u32x4>(lds.at[r][1][row] + from);
       if constexpr (kFmt == kFmtFp4) {
@@ -215,6 +246,20 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
     const unsigned long long ok = lds.ok[r];
     const bool clean = ragged && mixed_step(step, ok);
+    if constexpr (kDirect) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's rows are in LDS
+      if (ok == ~0ull && !clean) return;
+      // each lane puts right what it loaded
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) {
+        const int row = row0 + i * S::kRows;
+        u32x4* at = reinterpret_cast<u32x4*>(lds.v[b] + row * S::kStrideV + 16 * (tid % S::kLanes));
+        u32x4 x = *at;
+        if (clean) x = finite8<kFp16>(x, &special);
+        *at = (ok >> row) & 1ull ? x : u32x4{0u, 0u, 0u, 0u};
+      }
+      return;
+    }
     if (ok != ~0ull) {   // 0 * V must be 0 for keys that are not there
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i) {
@@ -234,17 +279,23 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     }
   };
 
-  if (p.dim < kDim) {   // the columns that no thread writes
+  if (!kFull) {   // the columns that no thread writes
     u32x4* const all = reinterpret_cast<u32x4*>(lds.k[0]);
     for (uint32_t i = tid; i < (sizeof(lds.k) + sizeof(lds.v)) / 16; i += kThreads)
       all[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
   }
   if (s_begin < s_end) {
-    place(s_begin, page_id(s_begin));
-    place(s_begin + 1, page_id(s_begin + 1));
+    const int32_t id0 = page_id(s_begin), id1 = page_id(s_begin + 1), id2 = page_id(s_begin + 2);
+    place(s_begin, id0);
+    const float scale0 = scale_late;
+    place(s_begin + 1, id1);
+    const float scale1 = scale_late;
+    place(s_begin + 2, id2);
+    put_scales(s_begin, scale0);
+    put_scales(s_begin + 1, scale1);
   }
-  int32_t page_next = page_id(s_begin + 2);
+  int32_t page_next = page_id(s_begin + 3);
   __syncthreads();
   if (s_begin < s_end) {
     load_rows(s_begin);
@@ -254,47 +305,57 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 
   for (int32_t step = s_begin; step < s_end; ++step) {
     const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
-    int32_t key0 = t.key_of(step);
+    const int32_t key0 = t.key_of(step);
     const bool more = step + 1 < s_end;
     if (more) load_rows(step + 1);
-    place(step + 2, page_next);
-    page_next = page_id(step + 3);
+    put_scales(step + 2, scale_late);
+    place(step + 3, page_next);
+    page_next = page_id(step + 4);
 
-    // S^T
-    f32x16 s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
-      const uint8_t* kp = lds.k[b] + (h * 32 + c32) * S::kStrideK + half * 16;
-#pragma unroll
-      for (int ks = 0; ks < kKs; ++ks)
-        s[h] = mfma32<kFp16>(*reinterpret_cast<const u32x4*>(kp + ks * 32), q[ks], s[h]);
-    }
-
-    // Key of value i of half h: key0 + 32 h + 8 (i / 4) + 4 half + i % 4.
+    // The step in 32-key halves, so that matrix and vector work of different
+    // halves overlap within the wave: while the second half's products run, the
+    // first's weights are worked out, and the other way round for V.
     const unsigned long long ok = lds.ok[r];
     const bool mixed = mixed_step(step, ok);
-    float vm[kFp8 ? 32 : 1];
+    // Rows 32 h + c32 of K; rows 16 k + 8 u + v_row of V (whose places are those
+    // of rows c32 and v_row).
+    const uint32_t v_row = 4 * half + (c16 >> 2);
+    const uint8_t* const kp = lds.k[b] + c32 * S::kStrideK;
+    uint8_t* const vp = lds.v[b] + v_row * S::kStrideV + 8 * (c16 & 1);
+    auto k_operand = [&](int h, int ks) {
+      const uint32_t at = 16 * ((2 * ks + half) ^ S::place_k(c32));
+      return *reinterpret_cast<const u32x4*>(kp + h * 32 * S::kStrideK + at);
+    };
+    auto v_operand = [&](int k, int dt) {
+      const uint32_t at = 16 * ((4 * dt + 2 * ((lane >> 4) & 1) + ((c16 >> 1) & 1)) ^ S::place_v(v_row));
+      const u32x2 x = read_column4(vp + (16 * k) * S::kStrideV + at);
+      const u32x2 y = read_column4(vp + (16 * k + 8) * S::kStrideV + at);
+      return u32x4{x.x, x.y, y.x, y.y};
+    };
+    u32x4 pt[4];          // P^T operands of 16 keys each
+    // Value i of half h: key key0 + 32 h + 8 (i / 4) + 4 half + i % 4.
+    f32x16 s[2];
+    uint32_t seen[2] = {~0u, ~0u};   // bit 8 (i / 4) + i % 4 of half h: the row sees value i
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < kKs; ++ks)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] = mfma32<kFp16>(k_operand(h, ks), q[ks], s[h]);
     if constexpr (kFp8) {
       if (dyn) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int at = 32 * h + 8 * j + 4 * half;
-            const f32x4 ks = *reinterpret_cast<const f32x4*>(&lds.scale[r][0][at]);
-            const f32x4 vs = *reinterpret_cast<const f32x4*>(&lds.scale[r][1][at]);
+            const f32x4 ks = *reinterpret_cast<const f32x4*>(&lds.scale[r][0][32 * h + 8 * j + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[h][4 * j + i] *= ks[i];
-              vm[16 * h + 4 * j + i] =
-                  __uint_as_float((__float_as_uint(vs[i]) & 0x807FFFFFu) | 0x3F800000u);
-            }
+            for (int i = 0; i < 4; ++i) s[h][4 * j + i] *= ks[i];
           }
       }
     }
-    uint32_t seen[2] = {~0u, ~0u};   // bit 8 (i / 4) + i % 4 of half h: the row sees value i
     if (mixed) {
       const unsigned long long bits = seen_bits(p, pos, key0, ok) >> (4 * half);
       seen[0] = (uint32_t)bits;
@@ -321,41 +382,42 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
     }
-    const float base = m == kNegInf ? 0.0f : -m;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
+    // Scores -> weights, two P^T operands.
+    auto weights_of = [&](int h, f32x16& s, uint32_t see) {
+      const float base = m == kNegInf ? 0.0f : -m;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], c, base));
-        l += s[h][i];
+        s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, base));
+        l += s[i];
       }
-    if constexpr (kFp8) {
-      if (dyn) {
+      if constexpr (kFp8) {
+        if (dyn) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 vs = *reinterpret_cast<const f32x4*>(&lds.v_sig[r][32 * h + 8 * j + 4 * half]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[h][i] = seen[h] & (1u << (8 * (i >> 2) + (i & 3))) ? s[h][i] * vm[16 * h + i] : 0.0f;
+            for (int i = 0; i < 4; ++i) s[4 * j + i] *= vs[i];
+          }
+          if (mixed) {    // the scale of a key that the row does not see may be anything
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? s[i] : 0.0f;
+          }
+        }
       }
-    }
-    u32x4 pt[4];   // P^T operands of 16 keys each
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int h = k >> 1, i = 8 * (k & 1);
-      pt[k] = u32x4{pack_pair<kFp16>(s[h][i], s[h][i + 1]), pack_pair<kFp16>(s[h][i + 2], s[h][i + 3]),
-                    pack_pair<kFp16>(s[h][i + 4], s[h][i + 5]), pack_pair<kFp16>(s[h][i + 6], s[h][i + 7])};
-    }
-
-    // O^T += V^T P^T
-    uint8_t* const vp = lds.v[b] + (4 * half + (c16 >> 2)) * S::kStrideV +
-                        (16 * ((lane >> 4) & 1) + 4 * (c16 & 3)) * 2;
-    auto v_operand = [&](int k, int dt) {
-      const u32x2 x = read_column4(vp + (16 * k) * S::kStrideV + dt * 64);
-      const u32x2 y = read_column4(vp + (16 * k + 8) * S::kStrideV + dt * 64);
-      return u32x4{x.x, x.y, y.x, y.y};
+      for (int k = 0; k < 2; ++k)
+        pt[2 * h + k] = u32x4{pack_pair<kFp16>(s[8 * k], s[8 * k + 1]), pack_pair<kFp16>(s[8 * k + 2], s[8 * k + 3]),
+                              pack_pair<kFp16>(s[8 * k + 4], s[8 * k + 5]), pack_pair<kFp16>(s[8 * k + 6], s[8 * k + 7])};
     };
+
+    weights_of(0, s[0], seen[0]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int dt = 0; dt < kDt; ++dt) acc[dt] = mfma32<kFp16>(v_operand(k, dt), pt[k], acc[dt]);
+    weights_of(1, s[1], seen[1]);
+#pragma unroll
+    for (int k = 2; k < 4; ++k)
 #pragma unroll
       for (int dt = 0; dt < kDt; ++dt) acc[dt] = mfma32<kFp16>(v_operand(k, dt), pt[k], acc[dt]);
 
@@ -383,7 +445,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int32_t d = d0 + dt * 32 + 8 * (i >> 2) + (i & 3);
-            if (d < p.dim) acc[dt][i] += special_at<kFmt, kFp16>(p, head, page, off, d);
+            if (d < dim) acc[dt][i] += special_at<kFmt, kFp16>(p, head, page, off, d);
           }
       }
     }
@@ -399,13 +461,13 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int d = dt * 32 + 8 * j + 4 * half;
-      if (d >= p.dim) continue;
+      if (d >= dim) continue;
       const f32x4 y = f32x4{acc[dt][4 * j], acc[dt][4 * j + 1], acc[dt][4 * j + 2], acc[dt][4 * j + 3]};
       if (n_splits == 1)
         *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
             u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
       else
-        *reinterpret_cast<f32x4*>(p.ws_o + at * p.dim + d) = y;
+        *reinterpret_cast<f32x4*>(p.ws_o + at * dim + d) = y;
     }
   if (n_splits > 1 && half == 0) {
     p.ws_ml[2 * at] = m;
@@ -440,9 +502,11 @@ int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) 
 
 int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int, hipStream_t stream) {
   const dim3 grid(p.tile_slots * p.kv_heads, (uint32_t)p.splits);
-  void (*kernel)(Params) = padded_dim == 64    ? kvattn_tile_kernel<64>
-                           : padded_dim == 128 ? kvattn_tile_kernel<128>
-                                               : kvattn_tile_kernel<256>;
+  const bool full = p.dim == padded_dim;
+  void (*kernel)(Params) =
+      padded_dim == 64    ? (full ? kvattn_tile_kernel<64, true> : kvattn_tile_kernel<64, false>)
+      : padded_dim == 128 ? (full ? kvattn_tile_kernel<128, true> : kvattn_tile_kernel<128, false>)
+                          : (full ? kvattn_tile_kernel<256, true> : kvattn_tile_kernel<256, false>);
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
   return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads * (kTileRows / kJoinRows)), p,
