@@ -36,6 +36,8 @@ constexpr int64_t kAttnTileBlocks = 256;
 // Fewest steps of a split: two for each of its four waves.
 constexpr int64_t kAttnMinChunk = 8;
 constexpr int64_t kAttnMostBlocks = (int64_t(1) << 24) - 1;
+// Keys of the last steps, and of those that are looked up ahead, stay below 2^31.
+constexpr int64_t kAttnMostKeys = INT32_MAX - 1024;
 constexpr int64_t kAttnMaxWorkspace = int64_t(1) << 30;
 
 int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c,
@@ -45,7 +47,7 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   if (c.num_heads <= 0 || c.head_dim <= 0 || c.head_dim > 256 || a.q_heads <= 0 ||
       a.q_heads % c.num_heads || c.page_size <= 0 || c.page_size > INT32_MAX || c.num_slots <= 0 ||
       c.num_slots < c.page_size || c.num_slots / c.page_size > INT32_MAX || a.max_pages == 0 ||
-      (int64_t)a.max_pages > INT32_MAX / c.page_size || a.max_len < 0 || a.window < 0 ||
+      (int64_t)a.max_pages > kAttnMostKeys / c.page_size || a.max_len < 0 || a.window < 0 ||
       a.sinks < 0 || !(a.sm_scale >= 0.0f) || !(a.sm_scale <= 3.4e38f))
     return KVSTORE_ERR_SHAPE;
   if (a.cu_q == nullptr && a.tokens != a.seqs) return KVSTORE_ERR_SHAPE;

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
   const uint32_t head = blockIdx.x % p.kv_heads;
   // later tiles of a sequence see more keys: they start first
   const uint32_t slot = p.tile_slots - 1 - blockIdx.x / p.kv_heads;
-  const uint32_t tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const uint32_t half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
   Tile<kStep> t;
   if (!tile_of(p, slot, kTileRows, &t)) return;
@@ -127,54 +127,57 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 
   // --- row addresses: threads 0-63 take a step's K rows, 64-127 its V rows ---
   const int32_t* table = p.table + (int64_t)t.seq * p.table_stride;
-  const bool is_v = w == 1;
+  const bool looks = w <= 1, is_v = w == 1;
+  const uint64_t page_bytes = is_v ? p.v.page : p.k.page, row_bytes = is_v ? p.v.offset : p.k.offset;
+  const uint64_t page_scales = is_v ? p.v.s_page : p.k.s_page;
+  const uint64_t row_scales = is_v ? p.v.s_offset : p.k.s_offset;
+  const uint64_t rows_at =
+      reinterpret_cast<uint64_t>(is_v ? p.v.data : p.k.data) + (int64_t)head * (is_v ? p.v.head : p.k.head);
+  const uint64_t scales_at =
+      reinterpret_cast<uint64_t>(is_v ? p.v.scales : p.k.scales) +
+      (kFmt == kFmtFp4 || p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * (is_v ? p.v.s_head : p.k.s_head)
+                                                            : 0);
   bool met_bad = false;
-  auto page_id = [&](int32_t step) -> int32_t {   // -2: no row of the tile sees the key
-    if (w > 1 || step >= s_end) return -2;
+  // Both loads below are made whether the key is one of the tile's or not, from a
+  // place that is there: loads under a condition would be waited for at once.
+  auto page_id = [&](int32_t step) -> int32_t {
     const int32_t key = t.key_of(step) + (int32_t)lane;
-    if (key >= t.end || (key < t.low && key >= p.sinks)) return -2;
     int32_t page, off;
-    key_page(p, key, &page, &off);
-    return table[page];
+    key_page(p, key < t.end ? key : t.end - 1, &page, &off);
+    return load_global<int32_t>(reinterpret_cast<uint64_t>(table + page));
   };
-  // A step's scales are loaded by place and written to LDS a step later, so that
-  // no step waits for them.
-  float scale_late = 1.0f;
-  auto put_scales = [&](int32_t step, float scale) {
+  // A step's scales are loaded by place and written to LDS a step later.
+  struct Scale {
+    float value;
+    bool there;
+  };
+  auto put_scales = [&](int32_t step, Scale x) {
     if constexpr (kFp8) {
-      if (w > 1 || step >= s_end) return;
       const int r = (step - s_begin) & (kRing - 1);
+      const float scale = dyn && x.there ? x.value : 1.0f;
       lds.scale[r][w][lane] = scale;
       if (is_v)
         lds.v_sig[r][lane] = __uint_as_float((__float_as_uint(scale) & 0x807FFFFFu) | 0x3F800000u);
     }
   };
-  auto place = [&](int32_t step, int32_t page) {
-    if (w > 1 || step >= s_end) return;
+  auto place = [&](int32_t step, int32_t page) -> Scale {
     const int32_t key = t.key_of(step) + (int32_t)lane;
     int32_t ignore, off;
     key_page(p, key, &ignore, &off);
-    const bool there = page >= 0 && page < p.num_pages;
-    met_bad = met_bad || (page != -2 && !there);
-    const Side& side = is_v ? p.v : p.k;
+    const bool want = step < s_end && key < t.end && (key >= t.low || key < p.sinks);
+    const bool there = want && (uint32_t)page < (uint32_t)p.num_pages;
+    met_bad = met_bad || (want && !there);
     const int r = (step - s_begin) & (kRing - 1);
     // Slot 0 stands in for keys that are not there: its row is loaded and not used.
-    const int64_t pg = there ? page : 0, of = there ? off : 0;
-    lds.at[r][w][lane] = reinterpret_cast<uint64_t>(side.data) + pg * side.page + of * side.offset +
-                         (int64_t)head * side.head;
-    const int64_t sc_at = pg * side.s_page + of * side.s_offset;
-    if constexpr (kFmt == kFmtFp4)
-      lds.scale_at[r][w][lane] =
-          reinterpret_cast<uint64_t>(side.scales) + sc_at + (int64_t)head * side.s_head;
-    if constexpr (kFp8) {
-      scale_late = 1.0f;
-      if (dyn && there)
-        scale_late = load_global<float>(
-            reinterpret_cast<uint64_t>(side.scales) + sc_at +
-            (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
-    }
+    const uint64_t pg = there ? (uint32_t)page : 0, of = there ? (uint32_t)off : 0;
+    const uint64_t sc_at = scales_at + pg * page_scales + of * row_scales;
+    lds.at[r][w][lane] = rows_at + pg * page_bytes + of * row_bytes;
+    if constexpr (kFmt == kFmtFp4) lds.scale_at[r][w][lane] = sc_at;
     const unsigned long long ok = __ballot(there);
     if (tid == 0) lds.ok[r] = ok;
+    Scale x = {1.0f, there};
+    if (dyn) x.value = load_global<float>(sc_at);
+    return x;
   };
 
   // --- rows: global memory -> registers -> LDS ---
@@ -184,25 +187,37 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
   // write nothing.
   const int32_t row0 = tid / S::kLanes, col = (tid % S::kLanes) * S::kElems;
   const bool writes = col < dim && row0 < kStep;
-  const int32_t from = writes ? (kFmt == kFmt16 ? 2 * col : kFmt == kFmtFp4 ? col / 2 : col) : 0;
+  const uint32_t piece = tid % S::kLanes;
+  const uint32_t from = writes ? (kFmt == kFmt16 ? 2 * col : kFmt == kFmtFp4 ? col / 2 : col) : 0;
   auto load_rows = [&](int32_t step) {
-    const int r = (step - s_begin) & (kRing - 1);
+    const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
+    // all addresses first: reads of LDS wait for loads into it
+    uint64_t k_at[S::kLoads], v_at[S::kLoads];
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int row = (row0 & (kStep - 1)) + i * S::kRows;
+      k_at[i] = lds.at[r][0][row] + (kDirect ? 16 * (piece ^ S::place_k(row)) : from);
+      v_at[i] = lds.at[r][1][row] + (kDirect ? 16 * (piece ^ S::place_v(row)) : from);
+    }
+    if constexpr (kDirect) {
+      // keeps the reads above from being moved down
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) asm volatile("" : "+v"(k_at[i]), "+v"(v_at[i]));
+    }
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int row = (row0 & (kStep - 1)) + i * S::kRows;
       if constexpr (kDirect) {
-        const int b = (step - s_begin) & 1;
-        const uint32_t piece = tid % S::kLanes;
         const int to = (i * S::kRows + w * (S::kRows / kWaves)) * S::kStrideK;   // of the wave
-        load_to_lds(lds.at[r][0][row] + 16 * (piece ^ S::place_k(row)), lds.k[b] + to);
-        load_to_lds(lds.at[r][1][row] + 16 * (piece ^ S::place_v(row)), lds.v[b] + to);
-        continue;
-      }
-      kr[i] = load_global<u32x4>(lds.at[r][0][row] + from);
-      vr[i] = load_global<u32x4>(lds.at[r][1][row] + from);
-      if constexpr (kFmt == kFmtFp4) {
-        kb[i] = load_global<uint8_t>(lds.scale_at[r][0][row] + (writes ? col / 32 : 0));
-        vb[i] = load_global<uint8_t>(lds.scale_at[r][1][row] + (writes ? col / 32 : 0));
+        load_to_lds(k_at[i], lds.k[b] + to);
+        load_to_lds(v_at[i], lds.v[b] + to);
+      } else {
+        kr[i] = load_global<u32x4>(k_at[i]);
+        vr[i] = load_global<u32x4>(v_at[i]);
+        if constexpr (kFmt == kFmtFp4) {
+          kb[i] = load_global<uint8_t>(lds.scale_at[r][0][row] + (writes ? col / 32 : 0));
+          vb[i] = load_global<uint8_t>(lds.scale_at[r][1][row] + (writes ? col / 32 : 0));
+        }
       }
     }
   };
@@ -253,7 +268,7 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i) {
         const int row = row0 + i * S::kRows;
-        u32x4* at = reinterpret_cast<u32x4*>(lds.v[b] + row * S::kStrideV + 16 * (tid % S::kLanes));
+        u32x4* at = reinterpret_cast<u32x4*>(lds.v[b] + row * S::kStrideV + 16 * piece);
         u32x4 x = *at;
         if (clean) x = finite8<kFp16>(x, &special);
         *at = (ok >> row) & 1ull ? x : u32x4{0u, 0u, 0u, 0u};
@@ -285,17 +300,16 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
       all[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
   }
-  if (s_begin < s_end) {
+  int32_t page_next = 0;
+  Scale scale_next = {1.0f, false};
+  if (s_begin < s_end && looks) {
     const int32_t id0 = page_id(s_begin), id1 = page_id(s_begin + 1), id2 = page_id(s_begin + 2);
-    place(s_begin, id0);
-    const float scale0 = scale_late;
-    place(s_begin + 1, id1);
-    const float scale1 = scale_late;
-    place(s_begin + 2, id2);
-    put_scales(s_begin, scale0);
-    put_scales(s_begin + 1, scale1);
+    page_next = page_id(s_begin + 3);
+    const Scale x = place(s_begin, id0), y = place(s_begin + 1, id1);
+    scale_next = place(s_begin + 2, id2);
+    put_scales(s_begin, x);
+    put_scales(s_begin + 1, y);
   }
-  int32_t page_next = page_id(s_begin + 3);
   __syncthreads();
   if (s_begin < s_end) {
     load_rows(s_begin);
@@ -307,10 +321,14 @@ __global__ __launch_bounds__(kThreads, kDim <= 128 ? 2 : 1) void kvattn_tile_ker
     const int b = (step - s_begin) & 1, r = (step - s_begin) & (kRing - 1);
     const int32_t key0 = t.key_of(step);
     const bool more = step + 1 < s_end;
+    // What this waits for was loaded a step ago; after load_rows it would wait for
+    // its loads, too.
+    if (looks) {
+      put_scales(step + 2, scale_next);
+      scale_next = place(step + 3, page_next);
+      page_next = page_id(step + 4);
+    }
     if (more) load_rows(step + 1);
-    put_scales(step + 2, scale_late);
-    place(step + 3, page_next);
-    page_next = page_id(step + 4);
 
     // The step in 32-key halves, so that matrix and vector work of different
     // halves overlap within the wave: while the second half's products run, the
