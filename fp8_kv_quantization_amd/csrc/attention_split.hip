@@ -193,7 +193,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
 
   u32x4 kr[2][S::kLoadsK], vr[S::kLoadsV];
   uint32_t kb[2][kFmt == kFmtFp4 ? S::kLoadsK : 1], vb[kFmt == kFmtFp4 ? S::kLoadsV : 1];
-  float sc = 1.0f;     // K's (lanes 0-31) or V's scale of key lane & 31
+  float sc = 1.0f;     // K's (lanes 0-31) or V's scale of key lane & 31, whether that is there or not
   uint32_t ok = 0;     // the step's keys that are there
 
   // Lanes past the head's dims load a row's start, and write or multiply nothing.
@@ -262,7 +262,6 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
         if (dyn) {
           const uint64_t base = lane < 32 ? (lane < 16 ? ksbase[0] : ksbase[1]) : (lane < 48 ? vsbase[0] : vsbase[1]);
           sc = load_global<float>(base + (int64_t)c16 * (lane < 32 ? p.k.s_offset : p.v.s_offset));
-          if (!((ok >> (lane & 31)) & 1u)) sc = 1.0f;
         }
       }
     } else {
@@ -280,8 +279,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
       const uint64_t scales = reinterpret_cast<uint64_t>(side.scales) + page * side.s_page + of * side.s_offset;
       if constexpr (kFmt == kFmtFp4) my.scale_at[lane >> 5][kk] = scales + (int64_t)head * side.s_head;
       if constexpr (kFp8) {
-        sc = 1.0f;
-        if (dyn && there)
+        if (dyn)
           sc = load_global<float>(scales + (p.scale_kind == KVATTN_TOKEN_HEAD ? (int64_t)head * side.s_head : 0));
       }
       __builtin_amdgcn_wave_barrier();
@@ -376,7 +374,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
     const uint32_t ok_now = ok;
     const bool mixed = mixed_step(key0);
     if constexpr (kFp8) {
-      if (dyn) my.scale[lane >> 5][lane & 31] = sc;
+      if (dyn) my.scale[lane >> 5][lane & 31] = (ok_now >> (lane & 31)) & 1u ? sc : 1.0f;
       __builtin_amdgcn_wave_barrier();
     }
     store_v(mixed);
