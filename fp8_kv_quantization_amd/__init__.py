@@ -386,10 +386,10 @@ def _tensor_calls():
     return _fast
 
 
-def _under(stream, call):
-    """`call` with `stream` current (None: the stream that is)."""
-    if stream is None:
-        return call()
+def _under(stream, device, call):
+    """`call` with `stream`, one of the tensors' device, current."""
+    if device.type == "cuda" and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with _torch().cuda.stream(stream):
         return call()
 
@@ -407,7 +407,7 @@ def store_kv_rope_paged(k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q
     scales as in store_kv_fp8_paged, 4-bit caches scale caches.  cos_sin None
     (with positions None): no rotation."""
     if stream is not None:
-        return _under(stream, lambda: store_kv_rope_paged(
+        return _under(stream, k.device, lambda: store_kv_rope_paged(
             k, v, k_cache, v_cache, cache_loc, positions, cos_sin, q, q_out, interleaved, page_size,
             inv_k_scale, inv_v_scale, k_scale_cache, v_scale_cache, size_limit))
     st = (_fast or _tensor_calls()).store_kv_rope_paged(
@@ -438,7 +438,7 @@ def load_kv_paged(k_cache, v_cache, cache_loc, k_out, v_out, page_size=16, k_sca
     [pages, page_size(, H)]; a row whose slot is out of range is left as it
     was and recorded."""
     if stream is not None:
-        return _under(stream, lambda: load_kv_paged(
+        return _under(stream, k_out.device, lambda: load_kv_paged(
             k_cache, v_cache, cache_loc, k_out, v_out, page_size, k_scale, v_scale, k_scale_cache,
             v_scale_cache, size_limit))
     st = (_fast or _tensor_calls()).load_kv_paged(
@@ -469,7 +469,9 @@ def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=
     q [T, Hq, D] holds the new tokens of B sequences, rows cu_q[b] ...
     cu_q[b + 1] - 1 those of sequence b (int32 [B + 1]; None: one each).
     seq_lens [B] int32 counts each sequence's keys, its new tokens' included;
-    page_table [B, pages] int32 names their pages.  A token at position p sees
+    page_table [B, pages] int32 names their pages.  Rows of out before cu_q[0]
+    and from cu_q[B] on are left as they were (uninitialised without `out`);
+    rows that see no key are 0.  There is no backward pass.  A token at position p sees
     the keys k <= p with p - k < window (0: all) or k < sinks.  max_q and
     max_len, the most new tokens and keys of a sequence where the caller knows
     them, only steer the launch.  workspace: a GPU tensor of the bytes that
@@ -477,7 +479,7 @@ def attention_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q=None, max_q=
     calls (or captured graphs) that may overlap need one each; by default the
     call takes one from torch's allocator."""
     if stream is not None:
-        return _under(stream, lambda: attention_paged(
+        return _under(stream, q.device, lambda: attention_paged(
             q, k_cache, v_cache, page_table, seq_lens, cu_q, max_q, max_len, window, sinks, sm_scale,
             page_size, k_scale, v_scale, k_scale_cache, v_scale_cache, out, workspace))
     got = (_fast or _tensor_calls()).attention_paged(

@@ -48,7 +48,7 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
       a.q_heads % c.num_heads || c.page_size <= 0 || c.page_size > INT32_MAX || c.num_slots <= 0 ||
       c.num_slots < c.page_size || c.num_slots / c.page_size > INT32_MAX || a.max_pages == 0 ||
       (int64_t)a.max_pages > kAttnMostKeys / c.page_size || a.max_len < 0 || a.window < 0 ||
-      a.sinks < 0 || !(a.sm_scale >= 0.0f) || !(a.sm_scale <= 3.4e38f))
+      a.sinks < 0 || !(a.sm_scale >= 0.0f) || !(a.sm_scale <= 2.3e38f))
     return KVSTORE_ERR_SHAPE;
   if (a.cu_q == nullptr && a.tokens != a.seqs) return KVSTORE_ERR_SHAPE;
   if ((int64_t)a.tokens * a.q_heads > INT32_MAX) return KVSTORE_ERR_SHAPE;
@@ -128,6 +128,7 @@ int kvstore_attention_paged(const kvstore_attention_args* args, const kvstore_pa
   const int fmt = row_fmt(c.format);
   if (fmt == kRow16 && fp16_format(c.format) != fp16) return KVSTORE_ERR_DTYPE;
   if (!a.q || !a.out || !a.page_table || !a.seq_lens) return KVSTORE_ERR_NULL;
+  if (a.q == a.out) return KVSTORE_ERR_SHAPE;
   AttentionPlan plan;
   st = plan_attention(a, c, &plan);
   if (st != KVSTORE_OK) return st;

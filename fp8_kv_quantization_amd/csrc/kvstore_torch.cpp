@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime_api.h>
@@ -19,6 +20,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <exception>
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -140,6 +142,14 @@ int64_t block_scales(const at::Tensor& t, bool paged, int64_t H, int64_t blocks,
   *page = t.stride(0);
   *offset = t.stride(1);
   return t.size(0) * page_size;
+}
+
+// None of the calls has a backward pass: tensors that wait for one are refused.
+void no_grad(std::initializer_list<Opt> tensors) {
+  if (!at::GradMode::is_enabled()) return;
+  for (Opt t : tensors)
+    if (t && t->requires_grad())
+      value_error("this call has no backward pass: detach tensors that require grad, or call it under torch.no_grad()");
 }
 
 struct Scales {
@@ -333,6 +343,7 @@ PyObject* rope(PyObject* const* a) {
   const int inter = PyObject_IsTrue(a[9]);
   if (inter < 0) throw AlreadySet();
   const float *pik = scalar(ik, "inverse scales"), *piv = scalar(iv, "inverse scales");
+  no_grad({&k, &v, &kc, &vc, table, q, q_out});
   Device dev;
   for (Opt t : {&k, &v, &kc, &vc, &loc, pos, table, q, q_out, ik, iv, scales.k_cache, scales.v_cache})
     dev.add(t);
@@ -368,6 +379,7 @@ PyObject* load(PyObject* const* a) {
   if (vo.size(0) != T) value_error("k_out and v_out must have the same rows");
   check_slots(loc, T);
   const int loc_dtype = idx_code(loc);
+  no_grad({&kc, &vc, &ko, &vo});
   Device dev;
   for (Opt t : {&kc, &vc, &loc, &ko, &vo, s.k_scale, s.v_scale, s.k_cache, s.v_cache}) dev.add(t);
   const uint32_t batch = batch_of(T);
@@ -417,6 +429,7 @@ PyObject* attention(PyObject* const* a) {
   if ((T > 0 && q.stride(2) != 1) || (out && T > 0 && out->stride(2) != 1))
     value_error("q and out must have a dim stride of 1");
   if (Hq > INT32_MAX || table.size(1) > UINT32_MAX) value_error("q or page_table is too wide");
+  no_grad({&q, &kc, &vc, s.k_scale, s.v_scale, s.k_cache, s.v_cache, out});
   r.q = q.data_ptr();
   r.q_stride_token = q.stride(0) * 2;
   r.q_stride_head = q.stride(1) * 2;

@@ -161,7 +161,8 @@ int kvstore_load_paged(const kvstore_paged_cache* cache, const void* indices, in
  * (window 0: all k <= p).  Key k lies in page page_table[b * table_stride + k
  * / page_size] at offset k % page_size.  For q head h, with kv head h /
  * (q_heads / num_heads):
- *   out = sum_k softmax_k(sm_scale * q . K_k) V_k,   0 where no key is seen.
+ *   out = sum_k softmax_k(sm_scale * q . K_k) V_k,   0 where no key is seen
+ * (or where every score is -infinity).
  * Keys that a row does not see never reach it, whatever their slots hold (NaN
  * and infinities included).  A page outside [0, num_slots / page_size) holds
  * no keys; the first row of every group of rows that meets it is recorded in
@@ -189,13 +190,13 @@ typedef struct kvstore_attention_args {
                                 Steers the launch only */
   const int32_t* page_table; /* [seqs, max_pages] */
   int64_t table_stride;      /* in elements */
-  uint32_t max_pages;        /* 0 < max_pages * page_size < 2^31 */
+  uint32_t max_pages;        /* 0 < max_pages * page_size < 2^31 - 1024 */
   const int32_t* seq_lens;   /* [seqs] */
   int64_t max_len;           /* longest sequence, if known; 0: max_pages * page_size.
                                 Steers the launch only */
   int64_t window;            /* >= 0 */
   int64_t sinks;             /* >= 0; not read if window is 0 */
-  float sm_scale;            /* >= 0, finite */
+  float sm_scale;            /* in [0, 2.3e38] */
   void* workspace;           /* kvstore_attention_workspace bytes, 16-byte aligned; in
                                 use until the call's work is done */
   int64_t workspace_bytes;
@@ -206,7 +207,8 @@ typedef struct kvstore_attention_args {
 int64_t kvstore_attention_workspace(const kvstore_attention_args* args,
                                     const kvstore_paged_cache* cache);
 
-/* head_dim is at most 256 here, page_size below 2^31. */
+/* head_dim is at most 256 here, page_size below 2^31, and num_slots holds at
+ * least one page. */
 int kvstore_attention_paged(const kvstore_attention_args* args, const kvstore_paged_cache* cache,
                             hipStream_t stream);
 
