@@ -42,6 +42,7 @@ struct Params {
   int32_t scale_kind;
   int32_t chunk_steps;     // steps of a split
   int32_t splits;          // splits that the workspace has room for
+  uint32_t join_parts;     // blocks of a tile in the kernel that joins splits
 };
 
 // Keys of a step of the split kernel and of the tile kernel, rows of a tile of

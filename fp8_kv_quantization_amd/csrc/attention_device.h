@@ -8,6 +8,7 @@ namespace kvattn {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -323,55 +324,85 @@ __device__ __forceinline__ Row row_of(const Params& p, const Tile<kStep>& t, uin
   return x;
 }
 
-// Joins the splits of each row: a wave per row, kJoinRows rows a block.  All of
-// a row's partial sums are loaded before any is needed.
-constexpr int kJoinRows = 4;
-template <bool kFp16, int kStep>
-__device__ __forceinline__ void join_splits(const Params& p, int32_t tile_rows, float v_scale) {
-  const uint32_t parts = tile_rows / kJoinRows;
-  const uint32_t part = blockIdx.x % parts, turn = blockIdx.x / parts;
-  const uint32_t head = turn % p.kv_heads, slot = turn / p.kv_heads;
-  Tile<kStep> t;
-  if (!tile_of(p, slot, tile_rows, &t)) return;
-  int32_t n_splits;
-  split_steps(p, t, &n_splits);
-  const int32_t r = part * kJoinRows + uniform(threadIdx.x >> 6);
-  if (n_splits == 1 || r >= t.rows) return;
-  const Row x = row_of(p, t, head, r);
+// Joins the splits of a row, by a wave, in one pass: its loads wait for nothing
+// but the sequence's length.
+template <bool kFp16>
+__device__ __forceinline__ void join_row(const Params& p, const Row& x, int32_t n_splits,
+                                         float v_scale) {
   const int64_t at = x.index * p.splits;
   const int32_t lane = threadIdx.x & 63;
   // lanes: four dims of a split each, as many splits side by side as fit
   const int32_t quads = p.dim / 4, side = 64 / quads;
   const int32_t d = lane % quads * 4, first = lane / quads;
-  float top = kNegInf;
-  for (int32_t i = lane; i < n_splits; i += 64) top = fmaxf(top, p.ws_ml[2 * (at + i)]);
-#pragma unroll
-  for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
-  float sum = 0.0f;
+  float top = kNegInf, sum = 0.0f;
   f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kAtOnce = 4;
   if (first < side) {
-#pragma unroll 4
-    for (int32_t i = first; i < n_splits; i += side) {
-      const float mi = p.ws_ml[2 * (at + i)], li = p.ws_ml[2 * (at + i) + 1];
-      const f32x4 o = *reinterpret_cast<const f32x4*>(p.ws_o + (at + i) * p.dim + d);
-      const float f = mi == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
-      sum += li * f;
+    for (int32_t i0 = first; i0 < n_splits; i0 += kAtOnce * side) {
+      float mi[kAtOnce], li[kAtOnce];
+      f32x4 o[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] += mi == kNegInf ? 0.0f : o[j] * f;
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int32_t i = i0 + e * side;
+        const int64_t from = at + (i < n_splits ? i : i0);
+        const f32x2 ml = *reinterpret_cast<const f32x2*>(p.ws_ml + 2 * from);
+        mi[e] = i < n_splits ? ml.x : kNegInf;
+        li[e] = ml.y;
+        o[e] = *reinterpret_cast<const f32x4*>(p.ws_o + from * p.dim + d);
+      }
+      float now = top;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) now = fmaxf(now, mi[e]);
+      const float keep = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+      top = now;
+      sum *= keep;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] *= keep;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const float f = mi[e] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mi[e] - now);
+        sum += mi[e] == kNegInf ? 0.0f : li[e] * f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] += mi[e] == kNegInf ? 0.0f : o[e][j] * f;
+      }
     }
   }
-  const float own_sum = sum;
-  const f32x4 own = y;
-  for (int32_t k = 1; k < side; ++k) {   // the other splits' lanes, in order
-    const int32_t from = lane % quads + k * quads;
-    sum += __shfl(own_sum, from);
+  if (side > 1) {   // the other splits' lanes, in order
+    float all = top;
+    for (int32_t k = 0; k < side; ++k) all = fmaxf(all, __shfl(top, lane % quads + k * quads));
+    const float f = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - all);
+    const float own_sum = sum * f;
+    const f32x4 own = f32x4{y[0] * f, y[1] * f, y[2] * f, y[3] * f};
+    sum = 0.0f;
+    y = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int32_t k = 0; k < side; ++k) {
+      const int32_t from = lane % quads + k * quads;
+      sum += __shfl(own_sum, from);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] += __shfl(own[j], from);
+      for (int j = 0; j < 4; ++j) y[j] += __shfl(own[j], from);
+    }
   }
   if (first > 0) return;
   const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
   *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
       u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
+}
+
+// Joins the splits of each row, kJoinRows rows a block at a time.
+constexpr int kJoinRows = 4;
+template <bool kFp16, int kStep>
+__device__ __forceinline__ void join_splits(const Params& p, int32_t tile_rows, float v_scale) {
+  const uint32_t part = blockIdx.x % p.join_parts, turn = blockIdx.x / p.join_parts;
+  const uint32_t head = turn % p.kv_heads, slot = turn / p.kv_heads;
+  Tile<kStep> t;
+  if (!tile_of(p, slot, tile_rows, &t)) return;
+  int32_t n_splits;
+  split_steps(p, t, &n_splits);
+  if (n_splits == 1) return;
+  // more rows than the host was told of take further turns
+  for (int32_t r = part * kJoinRows + uniform(threadIdx.x >> 6); r < t.rows;
+       r += p.join_parts * kJoinRows)
+    join_row<kFp16>(p, row_of(p, t, head, r), n_splits, v_scale);
 }
 
 }  // namespace kvattn

@@ -28,6 +28,7 @@ struct AttentionPlan {
   int32_t chunk_steps;
   int32_t splits;
   int64_t workspace;    // bytes
+  uint32_t join_parts;  // blocks of a tile in the kernel that joins splits
 };
 
 // Blocks to aim for (of 256 CUs' worth at a time, three or two a CU).
@@ -85,8 +86,9 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   if (row_bytes > 0 && splits > kAttnMaxWorkspace / row_bytes) splits = kAttnMaxWorkspace / row_bytes;
   const int64_t room = (kAttnMostBlocks / c.num_heads - 7) / (slots > 0 ? slots : 1);
   if (splits > room) splits = room;
-  // the kernel that joins splits has a block for every four rows
-  if (slots * c.num_heads > kAttnMostBlocks / (tile / 4)) splits = 1;
+  // the kernel that joins splits has a block for every four rows of a tile
+  plan->join_parts = (uint32_t)ceil_div(rows < tile ? rows : tile, 4);
+  if (slots * c.num_heads > kAttnMostBlocks / plan->join_parts) splits = 1;
   if (splits > 256) splits = 256;
   if (splits < 1) splits = 1;
   plan->chunk_steps = (int32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
@@ -180,6 +182,7 @@ int kvstore_attention_paged(const kvstore_attention_args* args, const kvstore_pa
   p.scale_kind = c.scale_kind;
   p.chunk_steps = plan.chunk_steps;
   p.splits = plan.splits;
+  p.join_parts = plan.join_parts;
   static const kvattn::Launch split[2][4] = {
       {kvattn::launch_split_bf16_0, kvattn::launch_split_bf16_1, kvattn::launch_split_bf16_2,
        kvattn::launch_split_bf16_3},

@@ -607,7 +607,7 @@ int launch_nr(const Params& p, int padded_dim, hipStream_t stream) {
     if (padded_dim == 256) kernel = kvattn_split_kernel<256, kNr, kWholePages, kFull>;
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
-  return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads * (16 * kNr / kJoinRows)), p,
+  return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads * p.join_parts), p,
              stream);
 }
 

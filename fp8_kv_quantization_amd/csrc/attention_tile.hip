@@ -527,7 +527,7 @@ int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int, hi
                           : (full ? kvattn_tile_kernel<256, true> : kvattn_tile_kernel<256, false>);
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
-  return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads * (kTileRows / kJoinRows)), p,
+  return run(kvattn_join_tiles_kernel, dim3(p.tile_slots * p.kv_heads * p.join_parts), p,
              stream);
 }
 
