@@ -45,31 +45,30 @@ struct Params {
   uint32_t join_parts;     // blocks of a tile in the kernel that joins splits
 };
 
-// Keys of a step of the split kernel and of the tile kernel, rows of a tile of
-// the latter.
+// Keys of a step and rows of a tile of the split kernel and of the tile kernel.
 constexpr int kSplitStep = 32;
+constexpr int kSplitRows = 16;
 constexpr int kTileStep = 64;
 constexpr int kTileRows = 128;
 
 // One per (source type, format); each returns a KVSTORE_* status.
-typedef int (*Launch)(const Params& p, int padded_dim, int nr, hipStream_t stream);
-// The split kernel for tiles of 16 * nr rows; the tile kernel (nr is not read).
-int launch_split_bf16_0(const Params&, int, int, hipStream_t);
-int launch_split_bf16_1(const Params&, int, int, hipStream_t);
-int launch_split_bf16_2(const Params&, int, int, hipStream_t);
-int launch_split_bf16_3(const Params&, int, int, hipStream_t);
-int launch_split_fp16_0(const Params&, int, int, hipStream_t);
-int launch_split_fp16_1(const Params&, int, int, hipStream_t);
-int launch_split_fp16_2(const Params&, int, int, hipStream_t);
-int launch_split_fp16_3(const Params&, int, int, hipStream_t);
+typedef int (*Launch)(const Params& p, int padded_dim, hipStream_t stream);
+int launch_split_bf16_0(const Params&, int, hipStream_t);
+int launch_split_bf16_1(const Params&, int, hipStream_t);
+int launch_split_bf16_2(const Params&, int, hipStream_t);
+int launch_split_bf16_3(const Params&, int, hipStream_t);
+int launch_split_fp16_0(const Params&, int, hipStream_t);
+int launch_split_fp16_1(const Params&, int, hipStream_t);
+int launch_split_fp16_2(const Params&, int, hipStream_t);
+int launch_split_fp16_3(const Params&, int, hipStream_t);
 
-int launch_tile_bf16_0(const Params&, int, int, hipStream_t);
-int launch_tile_bf16_1(const Params&, int, int, hipStream_t);
-int launch_tile_bf16_2(const Params&, int, int, hipStream_t);
-int launch_tile_bf16_3(const Params&, int, int, hipStream_t);
-int launch_tile_fp16_0(const Params&, int, int, hipStream_t);
-int launch_tile_fp16_1(const Params&, int, int, hipStream_t);
-int launch_tile_fp16_2(const Params&, int, int, hipStream_t);
-int launch_tile_fp16_3(const Params&, int, int, hipStream_t);
+int launch_tile_bf16_0(const Params&, int, hipStream_t);
+int launch_tile_bf16_1(const Params&, int, hipStream_t);
+int launch_tile_bf16_2(const Params&, int, hipStream_t);
+int launch_tile_bf16_3(const Params&, int, hipStream_t);
+int launch_tile_fp16_0(const Params&, int, hipStream_t);
+int launch_tile_fp16_1(const Params&, int, hipStream_t);
+int launch_tile_fp16_2(const Params&, int, hipStream_t);
+int launch_tile_fp16_3(const Params&, int, hipStream_t);
 
 }  // namespace kvattn

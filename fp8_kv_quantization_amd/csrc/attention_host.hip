@@ -21,7 +21,7 @@ unsigned long long* error_flag() {
 }
 
 struct AttentionPlan {
-  int nr;               // 16-row groups of a split tile; 0: the tile kernel
+  bool split;           // the split kernel (else the tile kernel)
   int padded_dim;
   uint32_t tile_slots;
   int32_t max_keys;
@@ -31,11 +31,29 @@ struct AttentionPlan {
   uint32_t join_parts;  // blocks of a tile in the kernel that joins splits
 };
 
-// Blocks to aim for (of 256 CUs' worth at a time, three or two a CU).
+// Up to 16 rows take the split kernel, which gets most out of few of them; more
+// take the tile kernel, which reads the cache once for up to 128 (32 rows, 8
+// sequences of 8192 keys, 8 kv heads of 128 dims: 54 us against the split
+// kernel's 110 in two passes over 16 bits, 61 against 94 over e4m3fn, 50 against
+// 56 over 4 bits).  16-bit rows of more than 64 dims go faster through the tile
+// kernel's loads into LDS, however few rows there are, once there is more to read
+// than kAttnTileBytes (one row of 4 heads a kv head, 8 kv heads of 128 dims: 8
+// sequences of 8192 keys 50 us against 70, 16 of 1024 21.0 against 23.4, one of
+// 8192 17.4 against 17.3, 4 of 2048 16 against 14.3, one of 777 14.8 against 10.8;
+// of 64 dims, 8 of 8192 34.3 against 33.9; e4m3fn, 8 of 8192: 58 against 47).
+constexpr int64_t kAttnTileBytes = int64_t(48) << 20;
+// Blocks to aim for by splits.  Split kernel: three or four a CU run at once, and
+// several turns of them even out sequences of different lengths (32 contexts of up
+// to 32768 4-bit keys: 167 us with 2048, 157 with 4096, 156 with 8192; 64 windows
+// of 4096: 106, 106, 109).  Tile kernel: the two a CU that run at once (single
+// rows over 8 x 8192 keys: 81 us with 256, 50 with 512, 60 with 768, 54 with 1024).
 constexpr int64_t kAttnSplitBlocks = 4096;
-constexpr int64_t kAttnTileBlocks = 256;
-// Fewest steps of a split: two for each of its four waves.
-constexpr int64_t kAttnMinChunk = 8;
+constexpr int64_t kAttnTileBlocks = 512;
+// Fewest steps of a split: one for each wave of a split block (777 keys of one
+// sequence: 10.4 us, 12.5 with half as many splits, 14.9 with a third), four of
+// the tile kernel's, whose prologue takes as long (32 rows over 512 keys: 15.8 us,
+// 18.8 with eight).
+constexpr int64_t kAttnMinChunk = 4;
 constexpr int64_t kAttnMostBlocks = (int64_t(1) << 24) - 1;
 // Keys of the last steps, and of those that are looked up ahead, stay below 2^31.
 constexpr int64_t kAttnMostKeys = INT32_MAX - 1024;
@@ -56,20 +74,23 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t group = a.q_heads / c.num_heads;
   const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q == 0 || a.max_q > a.tokens ? a.tokens : a.max_q;
   const int64_t rows = max_q * group;
-  // 64 rows of more than 128 dims do not fit a wave's registers
-  plan->nr = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 && c.head_dim <= 128 ? 4 : 0;
-  const int64_t step = plan->nr > 0 ? kvattn::kSplitStep : kvattn::kTileStep;
+  plan->max_keys = (int32_t)(a.max_pages * c.page_size);
+  int64_t keys = a.max_len > 0 && a.max_len < plan->max_keys ? a.max_len : plan->max_keys;
+  const int64_t seen = a.window > 0 && a.window < keys && a.sinks < keys - a.window ? a.window + a.sinks : keys;
+  const bool sixteen = c.format == KVSTORE_FMT_BF16 || c.format == KVSTORE_FMT_FP16;
+  plan->split = rows <= kvattn::kSplitRows &&
+                !(sixteen && c.head_dim > 64 &&
+                  seen > kAttnTileBytes / (4 * (int64_t)c.head_dim * c.num_heads) / a.seqs);
+  const int64_t step = plan->split ? kvattn::kSplitStep : kvattn::kTileStep;
   plan->padded_dim = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-  const int64_t tile = plan->nr > 0 ? 16 * plan->nr : kvattn::kTileRows;
+  const int64_t tile = plan->split ? kvattn::kSplitRows : kvattn::kTileRows;
   const int64_t slots = a.cu_q == nullptr ? a.seqs * ceil_div(group, tile)
                                           : (int64_t)a.tokens * group / tile + a.seqs;
   // blocks of 256 threads: a launch stays below 2^32 work-items (with its splits:
   // below)
   if ((slots + 7) * c.num_heads > kAttnMostBlocks) return KVSTORE_ERR_SHAPE;
   plan->tile_slots = (uint32_t)slots;
-  plan->max_keys = (int32_t)(a.max_pages * c.page_size);
   // Steps of a tile, at most (a longer sequence than max_len gets longer splits).
-  int64_t keys = a.max_len > 0 && a.max_len < plan->max_keys ? a.max_len : plan->max_keys;
   if (a.window > 0) {
     const int64_t span = a.window + (max_q < ceil_div(tile, group) ? max_q : ceil_div(tile, group)) +
                          a.sinks + 2 * step;
@@ -79,9 +100,9 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t tiles = a.cu_q == nullptr ? slots
                         : rows <= tile    ? (int64_t)a.seqs
                                           : (int64_t)a.tokens * group / tile + a.seqs / 2;
-  int64_t splits = ceil_div(plan->nr > 0 ? kAttnSplitBlocks : kAttnTileBlocks,
+  int64_t splits = ceil_div(plan->split ? kAttnSplitBlocks : kAttnTileBlocks,
                             (tiles > 0 ? tiles : 1) * c.num_heads);
-  if (splits > steps / kAttnMinChunk) splits = steps / kAttnMinChunk;
+  if (splits > ceil_div(steps, kAttnMinChunk)) splits = ceil_div(steps, kAttnMinChunk);
   const int64_t row_bytes = (int64_t)a.tokens * a.q_heads * (c.head_dim + 2) * 4;
   if (row_bytes > 0 && splits > kAttnMaxWorkspace / row_bytes) splits = kAttnMaxWorkspace / row_bytes;
   const int64_t room = (kAttnMostBlocks / c.num_heads - 7) / (slots > 0 ? slots : 1);
@@ -193,7 +214,7 @@ int kvstore_attention_paged(const kvstore_attention_args* args, const kvstore_pa
        kvattn::launch_tile_bf16_3},
       {kvattn::launch_tile_fp16_0, kvattn::launch_tile_fp16_1, kvattn::launch_tile_fp16_2,
        kvattn::launch_tile_fp16_3}};
-  return (plan.nr > 0 ? split : tile)[fp16][fmt](p, plan.padded_dim, plan.nr, stream);
+  return (plan.split ? split : tile)[fp16][fmt](p, plan.padded_dim, stream);
 }
 
 }  // extern "C"

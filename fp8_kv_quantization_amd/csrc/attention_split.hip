@@ -3,10 +3,10 @@
 //
 //   out = sum_k softmax_k(c q . K_k) V_k over the keys that a row sees.
 //
-// A block owns a tile of up to 16 * kNr rows (tokens x q heads of one kv head)
-// and one split of its keys.  Its four waves take the split's 32-key steps in
-// turn, each with a running maximum and sum of its own, and are joined through
-// LDS at the end; splits are joined by kvattn_join_kernel.
+// A block owns a tile of up to 16 rows (tokens x q heads of one kv head) and one
+// split of its keys.  Its four waves take the split's 32-key steps in turn, each
+// with a running maximum and sum of its own, and are joined through LDS at the
+// end; splits are joined by kvattn_join_kernel.
 //
 // Per step, S^T = K Q^T on 16x16x32 MFMAs: a K row's lanes load straight from
 // the cache into the operand's registers (the dims of a dot product may come in
@@ -21,6 +21,12 @@
 // until then weights stay below 2^8, exact enough in fp32 sums and in range in
 // either 16-bit type, and most steps skip the cross-lane maximum and the
 // rescaling of O.
+//
+// Bound by the latency of loads and the work of a step together: 32 contexts of
+// up to 32768 4-bit keys (32 q heads on 8 of 128 dims, 591 MB) take 157 us, 3.8
+// TB/s, and 102 us when all pages are the same few, in cache; 64 windows of 4096
+// e4m3fn keys (452 MB) 106 us, 4.3 TB/s, and 71 us.  One sequence of 777 bf16 keys
+// takes 10.4 us, two launches of serial latencies.
 #include "attention_device.h"
 #include "kvstore.h"
 
@@ -87,15 +93,14 @@ __device__ __forceinline__ uint32_t load_scalar(const int32_t* p) {
 // lie in one page: their rows have a scalar base and fixed lane offsets, and
 // page table reads are scalar loads.  Otherwise lanes look their keys' pages up
 // and hand the addresses over through LDS.  kFull: the head has kDim dims.
-template <int kDim, int kNr, bool kWholePages, bool kFull>
-__global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void kvattn_split_kernel(
+template <int kDim, bool kWholePages, bool kFull>
+__global__ __launch_bounds__(64 * kWaves, kDim <= 128 ? 3 : 1) void kvattn_split_kernel(
     const Params p) {
   typedef Shape<kDim> S;
-  constexpr int kTileRows = 16 * kNr;
   constexpr int kKs = kDim / 32;     // k steps of Q K^T
   constexpr int kDt = kDim / 16;     // column tiles of O
   __shared__ WaveLds<kDim, kWholePages> lds[kWaves];
-  __shared__ float s_m[kWaves][kTileRows], s_l[kWaves][kTileRows];
+  __shared__ float s_m[kWaves][kSplitRows], s_l[kWaves][kSplitRows];
 
   // Blocks go to the eight XCDs in turn.  The heads of one tile and split take
   // eight block numbers apart, so one XCD, which read the same cache lines where
@@ -110,7 +115,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
   const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const uint32_t g = lane >> 4, c16 = lane & 15;
   Tile<kStep> t;
-  if (!tile_of(p, slot, kTileRows, &t)) return;
+  if (!tile_of(p, slot, kSplitRows, &t)) return;
   int32_t n_splits;
   const int32_t chunk = split_steps(p, t, &n_splits);
   if ((int32_t)split >= n_splits) return;
@@ -127,33 +132,26 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
   }
 
   // Q^T operands and the positions of this lane's rows.
-  u32x4 q[kNr][kKs];
-  int32_t pos[kNr];
-#pragma unroll
-  for (int n = 0; n < kNr; ++n) {
-    const int32_t r = n * 16 + c16;
-    const int32_t row = t.row0 + (r < t.rows ? r : t.rows - 1);
+  u32x4 q[kKs];
+  int32_t pos;
+  {
+    const int32_t row = t.row0 + ((int32_t)c16 < t.rows ? (int32_t)c16 : t.rows - 1);
     const int32_t tok = row / (int32_t)p.group;
-    pos[n] = t.first_pos + tok;
+    pos = t.first_pos + tok;
     const uint8_t* src = p.q + (int64_t)(t.token0 + tok) * p.q_token +
                          (int64_t)(head * p.group + (row - tok * (int32_t)p.group)) * p.q_head;
 #pragma unroll
     for (int ks = 0; ks < kKs; ++ks) {
       const int d = (ks / S::kEB) * 32 * S::kEB + g * 8 * S::kEB + (ks % S::kEB) * 8;
-      q[n][ks] = u32x4{0u, 0u, 0u, 0u};
-      if (d < dim) q[n][ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
+      q[ks] = u32x4{0u, 0u, 0u, 0u};
+      if (d < dim) q[ks] = *reinterpret_cast<const u32x4*>(src + 2 * d);
     }
   }
 
-  f32x4 acc[kDt][kNr];
-  float m[kNr], l[kNr];
+  f32x4 acc[kDt];
+  float m = kNegInf, l = 0.0f;
 #pragma unroll
-  for (int n = 0; n < kNr; ++n) {
-    m[n] = kNegInf;
-    l[n] = 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < kDt; ++dt) acc[dt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int dt = 0; dt < kDt; ++dt) acc[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t* table = p.table + (int64_t)t.seq * p.table_stride;
   const int64_t head_k = (int64_t)head * p.k.head, head_v = (int64_t)head * p.v.head;
@@ -380,11 +378,10 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
     store_v(mixed);
 
     // S^T, in 16-key halves.
-    f32x4 s[2][kNr];
+    f32x4 s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < kNr; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < kKs; ++ks) {
 #pragma unroll
@@ -403,8 +400,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
         }
         // q is 0 past the head's dims; what was loaded in their place need not be finite
         if (!kFull && dk + (ks / kEB) * 32 * kEB + e * 8 >= dim) a = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int n = 0; n < kNr; ++n) s[h][n] = mfma16<kFp16>(a, q[n][ks], s[h][n]);
+        s[h] = mfma16<kFp16>(a, q[ks], s[h]);
       }
     }
 
@@ -429,50 +425,47 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
       next = pages_of(min(step + 2 * kWaves, s_end - 1));
     }
 
-    u32x4 pt[kNr];        // P^T operand
+    float x[8];
+    float top = kNegInf;
 #pragma unroll
-    for (int n = 0; n < kNr; ++n) {
-      float x[8];
-      float top = kNegInf;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 4; ++i)
+        x[4 * h + i] = s[h][i] * (dyn ? c * ksc[h][i] : c);
+    uint32_t seen = ~0u;   // bits i and 16 + i: the row sees the lane's key i of half 0 and 1
+    if (mixed) {
+      seen = (uint32_t)seen_bits(p, pos, key0, ok_now) >> (4 * g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[4 * h + i] = s[h][n][i] * (dyn ? c * ksc[h][i] : c);
-      uint32_t seen = ~0u;   // bits i and 16 + i: the row sees the lane's key i of half 0 and 1
-      if (mixed) {
-        seen = (uint32_t)seen_bits(p, pos[n], key0, ok_now) >> (4 * g);
+      for (int i = 0; i < 8; ++i) x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? x[i] : kNegInf;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? x[i] : kNegInf;
-      }
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+    if (__ballot(top > m + kLazy || (m == kNegInf && top > kNegInf)) != 0) {
+      const float was = m, now = fmaxf(was, group_max4(top));
+      const float f = now == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(was - now);
+      m = now;
+      l *= f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
-      if (__ballot(top > m[n] + kLazy || (m[n] == kNegInf && top > kNegInf)) != 0) {
-        const float was = m[n], now = fmaxf(was, group_max4(top));
-        const float f = now == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(was - now);
-        m[n] = now;
-        l[n] *= f;
+      for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
-        for (int dt = 0; dt < kDt; ++dt)
+        for (int i = 0; i < 4; ++i) acc[dt][i] *= f;
+    }
+    const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[dt][n][i] *= f;
-      }
-      const float base = m[n] == kNegInf ? 0.0f : m[n];
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+      l += x[i];
+    }
+    if (dyn) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(x[i] - base);
-        l[n] += x[i];
+        const float y = x[i] * vsc[i >> 2][i & 3];
+        x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? y : 0.0f;
       }
-      if (dyn) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = x[i] * vsc[i >> 2][i & 3];
-          x[i] = seen & (1u << ((i >> 2) * 16 + (i & 3))) ? y : 0.0f;
-        }
-      }
-      pt[n] = u32x4{pack_pair<kFp16>(x[0], x[1]), pack_pair<kFp16>(x[2], x[3]),
-                    pack_pair<kFp16>(x[4], x[5]), pack_pair<kFp16>(x[6], x[7])};
     }
+    const u32x4 pt =    // P^T operand
+        u32x4{pack_pair<kFp16>(x[0], x[1]), pack_pair<kFp16>(x[2], x[3]),
+              pack_pair<kFp16>(x[4], x[5]), pack_pair<kFp16>(x[6], x[7])};
 
     // O^T += V^T P^T.
     __builtin_amdgcn_wave_barrier();
@@ -482,8 +475,7 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
       const u32x2 a = read_column4(col + dt * 32);
       const u32x2 b = read_column4(col + 16 * S::kStrideV + dt * 32);
       const u32x4 vt = u32x4{a.x, a.y, b.x, b.y};
-#pragma unroll
-      for (int n = 0; n < kNr; ++n) acc[dt][n] = mfma16<kFp16>(vt, pt[n], acc[dt][n]);
+      acc[dt] = mfma16<kFp16>(vt, pt, acc[dt]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -509,84 +501,73 @@ __global__ __launch_bounds__(64 * kWaves, kNr == 1 && kDim <= 128 ? 3 : 1) void 
           for (int i = 0; i < 4; ++i) {
             if (d0 + dt * 16 + i >= dim) continue;
             const float x = special_at<kFmt, kFp16>(p, head, page, off, d0 + dt * 16 + i);
-#pragma unroll
-            for (int n = 0; n < kNr; ++n) acc[dt][n][i] += sees(p, pos[n], key) ? x : 0.0f;
+            acc[dt][i] += sees(p, pos, key) ? x : 0.0f;
           }
       }
     }
   }
 
   // Join the waves.
-#pragma unroll
-  for (int n = 0; n < kNr; ++n) {
-    l[n] += __shfl_xor(l[n], 16);
-    l[n] += __shfl_xor(l[n], 32);
-    if (g == 0) {
-      s_m[w][n * 16 + c16] = m[n];
-      s_l[w][n * 16 + c16] = l[n];
-    }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    s_m[w][c16] = m;
+    s_l[w][c16] = l;
   }
   __syncthreads();
+  float top = kNegInf;
 #pragma unroll
-  for (int n = 0; n < kNr; ++n) {
-    if (n > 0) __syncthreads();
-    if (n * 16 >= t.rows) return;   // the whole block
-    float top = kNegInf;
+  for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_m[i][c16]);
+  const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  float* o = reinterpret_cast<float*>(my.v) + c16 * S::kStrideO + 4 * g;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_m[i][n * 16 + c16]);
-    const float f = m[n] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
-    float* o = reinterpret_cast<float*>(my.v) + c16 * S::kStrideO + 4 * g;
+  for (int dt = 0; dt < kDt; ++dt) {
+    f32x4 y;
 #pragma unroll
-    for (int dt = 0; dt < kDt; ++dt) {
-      f32x4 y;
+    for (int i = 0; i < 4; ++i) y[i] = acc[dt][i] * f;
+    *reinterpret_cast<f32x4*>(o + dt * 16) = y;
+  }
+  __syncthreads();
+  // 16 threads per row, four columns at a time
+  const int r = threadIdx.x >> 4, part = threadIdx.x & 15;
+  if (r < t.rows) {
+    float row_top = kNegInf, row_l = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = acc[dt][n][i] * f;
-      *reinterpret_cast<f32x4*>(o + dt * 16) = y;
+    for (int i = 0; i < kWaves; ++i) row_top = fmaxf(row_top, s_m[i][r]);
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      const float mi = s_m[i][r];
+      row_l += mi == kNegInf ? 0.0f : s_l[i][r] * __builtin_amdgcn_exp2f(mi - row_top);
     }
-    __syncthreads();
-    // 16 threads per row, four columns at a time
-    const int r = threadIdx.x >> 4, part = threadIdx.x & 15;
-    if (n * 16 + r < t.rows) {
-      float row_top = kNegInf, row_l = 0.0f;
+    const Row x = row_of(p, t, head, r);
+    const int64_t at = x.index * p.splits + split;
+    const float inv = row_l == 0.0f ? 0.0f : v_scale / row_l;
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) row_top = fmaxf(row_top, s_m[i][n * 16 + r]);
+    for (int d = part * 4; d < kDim; d += 64) {
+      f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        const float mi = s_m[i][n * 16 + r];
-        row_l += mi == kNegInf ? 0.0f : s_l[i][n * 16 + r] * __builtin_amdgcn_exp2f(mi - row_top);
+      for (int i = 0; i < kWaves; ++i)
+        y += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[i].v) +
+                                             r * S::kStrideO + d);
+      if (d >= dim) continue;
+      if (n_splits == 1) {
+        *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
+            u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
+      } else {
+        *reinterpret_cast<f32x4*>(p.ws_o + at * dim + d) = y;
       }
-      const Row x = row_of(p, t, head, n * 16 + r);
-      const int64_t at = x.index * p.splits + split;
-      const float inv = row_l == 0.0f ? 0.0f : v_scale / row_l;
-#pragma unroll
-      for (int d = part * 4; d < kDim; d += 64) {
-        f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i)
-          y += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[i].v) +
-                                               r * S::kStrideO + d);
-        if (d >= dim) continue;
-        if (n_splits == 1) {
-          *reinterpret_cast<u32x2*>(p.out + x.token * p.o_token + (int64_t)x.head * p.o_head + 2 * d) =
-              u32x2{pack_pair<kFp16>(y[0] * inv, y[1] * inv), pack_pair<kFp16>(y[2] * inv, y[3] * inv)};
-        } else {
-          *reinterpret_cast<f32x4*>(p.ws_o + at * dim + d) = y;
-        }
-      }
-      if (n_splits > 1 && part == 0) {
-        p.ws_ml[2 * at] = row_top;
-        p.ws_ml[2 * at + 1] = row_l;
-      }
+    }
+    if (n_splits > 1 && part == 0) {
+      p.ws_ml[2 * at] = row_top;
+      p.ws_ml[2 * at + 1] = row_l;
     }
   }
 }
 
-template <int kNr>
 __global__ __launch_bounds__(256) void kvattn_join_kernel(const Params p) {
-  const bool tensor = (kFmt == kFmtE4M3 || kFmt == kFmtE5M2) && p.scale_kind == KVATTN_TENSOR;
-  join_splits<kFp16, kStep>(p, 16 * kNr, tensor && p.v.scales
-                                             ? *reinterpret_cast<const float*>(p.v.scales)
-                                             : 1.0f);
+  join_splits<kFp16, kStep>(p, kSplitRows, kFp8 && p.scale_kind == KVATTN_TENSOR && p.v.scales
+                                               ? *reinterpret_cast<const float*>(p.v.scales)
+                                               : 1.0f);
 }
 
 int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) {
@@ -598,29 +579,15 @@ int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) 
              : KVSTORE_ERR_HIP;
 }
 
-template <int kNr, bool kWholePages, bool kFull>
-int launch_nr(const Params& p, int padded_dim, hipStream_t stream) {
+template <bool kWholePages, bool kFull>
+int launch_dims(const Params& p, int padded_dim, hipStream_t stream) {
   const dim3 grid((p.tile_slots * p.splits + 7) / 8 * 8 * p.kv_heads);
-  void (*kernel)(Params) = padded_dim == 64 ? kvattn_split_kernel<64, kNr, kWholePages, kFull>
-                                            : kvattn_split_kernel<128, kNr, kWholePages, kFull>;
-  if constexpr (kNr < 4)   // the host asks for 64 rows up to 128 dims only
-    if (padded_dim == 256) kernel = kvattn_split_kernel<256, kNr, kWholePages, kFull>;
+  void (*kernel)(Params) = padded_dim == 64    ? kvattn_split_kernel<64, kWholePages, kFull>
+                           : padded_dim == 128 ? kvattn_split_kernel<128, kWholePages, kFull>
+                                               : kvattn_split_kernel<256, kWholePages, kFull>;
   const int st = run(kernel, grid, p, stream);
   if (st != KVSTORE_OK || p.splits == 1) return st;
-  return run(kvattn_join_kernel<kNr>, dim3(p.tile_slots * p.kv_heads * p.join_parts), p,
-             stream);
-}
-
-template <int kNr>
-int launch_pages(const Params& p, int padded_dim, hipStream_t stream) {
-  // Whole pages: 32-bit strides, and 32-bit offsets of lanes into 16 rows.
-  const int64_t most = INT32_MAX / 32;
-  const bool whole = p.page_size % 16 == 0 && p.k.offset <= most && p.v.offset <= most &&
-                     p.k.s_offset <= most && p.v.s_offset <= most && p.k.page <= INT32_MAX &&
-                     p.v.page <= INT32_MAX && p.k.s_page <= INT32_MAX && p.v.s_page <= INT32_MAX;
-  if (!whole) return launch_nr<kNr, false, false>(p, padded_dim, stream);
-  return p.dim == padded_dim ? launch_nr<kNr, true, true>(p, padded_dim, stream)
-                             : launch_nr<kNr, true, false>(p, padded_dim, stream);
+  return run(kvattn_join_kernel, dim3(p.tile_slots * p.kv_heads * p.join_parts), p, stream);
 }
 
 }  // namespace
@@ -633,13 +600,15 @@ int launch_pages(const Params& p, int padded_dim, hipStream_t stream) {
 #define KVATTN_SRC bf16
 #endif
 
-int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int nr,
-                                        hipStream_t stream) {
-  switch (nr) {
-    case 1: return launch_pages<1>(p, padded_dim, stream);
-    case 2: return launch_pages<2>(p, padded_dim, stream);
-    default: return launch_pages<4>(p, padded_dim, stream);
-  }
+int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, hipStream_t stream) {
+  // Whole pages: 32-bit strides, and 32-bit offsets of lanes into 16 rows.
+  const int64_t most = INT32_MAX / 32;
+  const bool whole = p.page_size % 16 == 0 && p.k.offset <= most && p.v.offset <= most &&
+                     p.k.s_offset <= most && p.v.s_offset <= most && p.k.page <= INT32_MAX &&
+                     p.v.page <= INT32_MAX && p.k.s_page <= INT32_MAX && p.v.s_page <= INT32_MAX;
+  if (!whole) return launch_dims<false, false>(p, padded_dim, stream);
+  return p.dim == padded_dim ? launch_dims<true, true>(p, padded_dim, stream)
+                             : launch_dims<true, false>(p, padded_dim, stream);
 }
 
 }  // namespace kvattn

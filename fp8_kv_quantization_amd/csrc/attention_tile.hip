@@ -518,7 +518,7 @@ int run(void (*kernel)(Params), dim3 grid, const Params& p, hipStream_t stream) 
 #define KVATTN_SRC bf16
 #endif
 
-int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, int, hipStream_t stream) {
+int KVATTN_NAME(KVATTN_SRC, KVATTN_FMT)(const Params& p, int padded_dim, hipStream_t stream) {
   const dim3 grid(p.tile_slots * p.kv_heads, (uint32_t)p.splits);
   const bool full = p.dim == padded_dim;
   void (*kernel)(Params) =

@@ -196,3 +196,25 @@ def test_in_place_attention_is_refused():
     c = Case(70, lens=[64], new=1)
     with pytest.raises(kv.KVStoreError):
         c(out=c.q)
+
+
+@pytest.mark.parametrize("D", [80, 128, 256])
+@pytest.mark.parametrize("P", [16, 7])
+@pytest.mark.parametrize("lens", [[1, 0, 63], [64, 65, 900], [2500, 128, 3]])
+def test_single_tokens_where_much_may_be_read(D, P, lens):
+    """Tables wide enough for long contexts, whatever the sequences hold."""
+    rng = np.random.default_rng(D + P)
+    cache = Cache(rng, "bf16", pages_for(lens, P), P, 2, D, "tensor")
+    table = make_table(rng, cache, lens, spare=60000 // P)
+    q = queries(rng, 3, 8, D, "bf16")
+    out = kv.attention_paged(q, cache.k, cache.v, dev(table), dev(np.array(lens, np.int32)), **cache.kwargs())
+    ref, parts = attention(q.double().cpu().numpy(), cache, table, lens, [0, 1, 2, 3])
+    assert_attention(out, ref, parts, "bf16")
+    assert check_flag() == (kv.OK, -1, 0)
+
+
+@pytest.mark.parametrize("new", [4, 5, 33])
+@pytest.mark.parametrize("fmt,kind", [("bf16", "tensor"), ("e5m2", "token"), ("fp4", "block")])
+def test_short_runs_over_long_contexts(new, fmt, kind):
+    c = Case(80 + new, lens=[6000, 40, 1111], new=new, fmt=fmt, kind=kind)
+    c.check(c(max_q=new, max_len=6000))
