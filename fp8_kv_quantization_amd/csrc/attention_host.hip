@@ -46,7 +46,8 @@ constexpr int64_t kAttnTileBytes = int64_t(48) << 20;
 // several turns of them even out sequences of different lengths (32 contexts of up
 // to 32768 4-bit keys: 167 us with 2048, 157 with 4096, 156 with 8192; 64 windows
 // of 4096: 106, 106, 109).  Tile kernel: the two a CU that run at once (single
-// rows over 8 x 8192 keys: 81 us with 256, 50 with 512, 60 with 768, 54 with 1024).
+// rows over 8 x 8192 keys: 81 us with 256, 50 with 512, 60 with 768, 54 with 1024),
+// and no more (6 prompt chunks, 372 blocks of some 35 steps: 84 us whole, 88 in two).
 constexpr int64_t kAttnSplitBlocks = 4096;
 constexpr int64_t kAttnTileBlocks = 512;
 // Fewest steps of a split: one for each wave of a split block (777 keys of one
@@ -100,8 +101,9 @@ int plan_attention(const kvstore_attention_args& a, const kvstore_paged_cache& c
   const int64_t tiles = a.cu_q == nullptr ? slots
                         : rows <= tile    ? (int64_t)a.seqs
                                           : (int64_t)a.tokens * group / tile + a.seqs / 2;
-  int64_t splits = ceil_div(plan->split ? kAttnSplitBlocks : kAttnTileBlocks,
-                            (tiles > 0 ? tiles : 1) * c.num_heads);
+  const int64_t whole = (tiles > 0 ? tiles : 1) * c.num_heads;   // blocks without splits
+  int64_t splits = plan->split ? ceil_div(kAttnSplitBlocks, whole) : kAttnTileBlocks / whole;
+  if (splits < 1) splits = 1;
   if (splits > ceil_div(steps, kAttnMinChunk)) splits = ceil_div(steps, kAttnMinChunk);
   const int64_t row_bytes = (int64_t)a.tokens * a.q_heads * (c.head_dim + 2) * 4;
   if (row_bytes > 0 && splits > kAttnMaxWorkspace / row_bytes) splits = kAttnMaxWorkspace / row_bytes;

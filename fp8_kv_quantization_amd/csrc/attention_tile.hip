@@ -1,25 +1,38 @@
-// Paged attention for many rows (prompts and chunks of them): compiled once per
-// source type and cache format (KVATTN_FP16, KVATTN_FMT).
+// Paged attention for many rows (prompts, chunks of them, short runs), and for few
+// where a 16-bit cache has much to read: compiled once per source type and cache
+// format (KVATTN_FP16, KVATTN_FMT).
 //
 //   out = sum_k softmax_k(c q . K_k) V_k over the keys that a row sees.
 //
 // A block owns 128 rows (tokens x q heads of one kv head, so that the heads of
 // a group share the keys that the block reads) and walks their keys in steps of
 // 64; each of its four waves has 32 rows.  K and V go through LDS as 16-bit
-// values, double-buffered: the next step's rows are loaded into registers
-// before a step's products and converted and written behind them, with one
-// barrier a step.  The addresses of a step's rows (page table lookups) are
-// worked out two steps ahead, one key a thread, and handed over through LDS.
+// values, double-buffered: the next step's rows are on their way during a step's
+// products (16 bits: straight into LDS; others in registers, converted and
+// written behind the products), with one barrier a step.  The addresses of a
+// step's rows (page table lookups) are worked out three steps ahead, one key a
+// thread, and handed over through LDS.
 //
 // S^T = K Q^T on 32x32x16 MFMAs; a lane then holds keys of one row only, so the
 // softmax needs one exchange between two lanes, and its weights are in place
 // as the operand P^T of O^T = V^T P^T once the keys of V are taken in the same
 // order: four consecutive ones at a time, by transposing reads.
 //
-// Bound by the matrix cores and the softmax's vector work, which are of equal
-// size at 128 dims (per 64 keys and 32 rows: 1024 cycles of MFMA; 32 exponentials
-// at quarter rate and some 100 other operations, 900 cycles); two waves a SIMD
-// overlap the two.
+// The running maximum is raised only when a score exceeds it by more than 2^8, as
+// in the split kernel.
+//
+// Bound, at 128 dims, by a step's serial parts: 32 MFMAs (1024 cycles a wave), 32
+// exponentials at quarter rate and some 150 other vector operations, reads of 32
+// KB of LDS for each wave, two waves a SIMD.  A prompt of 8192 bf16 tokens (32 q
+// heads on 8 of 128 dims, 550 GFLOP) takes 610-630 us, 0.87-0.90 PFLOP/s, where a
+// matrix product of 8192^3 reaches 1.25; without the softmax it takes 0.93 of
+// that time, without LDS reads 0.85, without loads and lookups 0.83, without all
+// three 0.55.  Chunks of 2048 tokens over 8192 4-bit keys (324 GFLOP) take 366
+// us.  Six chunks of up to 1024 tokens in windows of 2048 e4m3fn keys with a scale
+// for each token and head (64 dims, 22 GFLOP) take 84 us: 372 blocks of 35 steps,
+// 5300 cycles each, of which the lookup of addresses and scales takes 900 in the
+// two waves that do it (the others wait), the products of Q and K 1000, the
+// softmax and the products with V 1800, the conversion of the next rows 900.
 #include "attention_device.h"
 #include "kvstore.h"
 

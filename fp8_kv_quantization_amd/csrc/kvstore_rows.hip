@@ -6,6 +6,12 @@
 // once, converted in registers and written once.  A lane works on one 8-element
 // chunk (16 bytes of 16-bit values) of kHeads consecutive heads of a token, so
 // a wave access covers whole 128-byte lines of each head.
+//
+// Measured: 16384 tokens of 32 q and 8 kv heads of 128 bf16 dims, rotated, into an
+// e4m3fn cache (378 MB) 69 us, 5.5 TB/s (a large device copy reaches 4.9); 8192
+// into a 4-bit cache and back out 49.7 us for 224 MB (42 and 10 us); 16384 rows of 8
+// heads out of an e4m3fn cache with a scale for each token and head (102 MB) 21
+// us; 16 tokens of a decode step 3.4 us, the cost of a launch.
 
 #include "kvstore_paged.h"
 
@@ -521,6 +527,10 @@ void fill_rows(RowsParams& r, const kvstore_paged_cache& c, const void* indices,
 
 // Heads per lane: four for long batches (their loads are in flight together
 // and share the cosines), one where that would leave CUs without a wave.
+// Appended tokens of 32 + 2 x 8 heads of 128 dims, one head a lane / four: 16
+// tokens 3.3 / 4.6 us, 256 3.5 / 4.9, 1024 7.6 / 7.3, 4096 21.9 / 19.5, 16384
+// 78.2 / 60.8; loaded tokens of 2 x 8: 1024 3.5 / 4.5, 4096 6.7 / 6.5, 16384
+// 18.8 / 15.1.
 constexpr int kRowsHeads = 4;
 constexpr int64_t kRowsManyWaves = 2048;
 
