@@ -218,3 +218,30 @@ def test_single_tokens_where_much_may_be_read(D, P, lens):
 def test_short_runs_over_long_contexts(new, fmt, kind):
     c = Case(80 + new, lens=[6000, 40, 1111], new=new, fmt=fmt, kind=kind)
     c.check(c(max_q=new, max_len=6000))
+
+
+@pytest.mark.parametrize("P", [16, 10])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (24600, 5)])
+def test_unseen_nan_where_much_is_read(P, window, sinks):
+    """Single tokens over long 16-bit contexts: slots that no token sees hold NaN
+    and infinity."""
+    rng = np.random.default_rng(P + window)
+    lens, D = [25000, 24700], 128
+    cache = Cache(rng, "bf16", pages_for(lens, P), P, 2, D, "tensor")
+    table = make_table(rng, cache, lens)
+    unseen = np.ones((cache.pages, P), bool)
+    for b, n in enumerate(lens):
+        for k in list(range(min(sinks, n))) + list(range(max(0, n - window) if window else 0, n)):
+            unseen[table[b, k // P], k % P] = False
+    where = torch.from_numpy(unseen)
+    for t in cache.tensors:
+        h = t.cpu()
+        h[where] = torch.tensor([float("nan"), float("inf")]).repeat(D // 2).to(h.dtype)
+        t.copy_(h)
+    q = queries(rng, 2, 4, D, "bf16")
+    out = kv.attention_paged(q, cache.k, cache.v, dev(table), dev(np.array(lens, np.int32)), window=window,
+                             sinks=sinks, **cache.kwargs())
+    ref, parts = attention(q.double().cpu().numpy(), cache, table, lens, [0, 1, 2], window, sinks)
+    assert np.isfinite(ref).all()
+    assert_attention(out, ref, parts, "bf16")
+    assert check_flag() == (kv.OK, -1, 0)
