@@ -1,5 +1,5 @@
-// Paged attention for few rows (single tokens, short runs, and chunks of long
-// ones): compiled once per source type and cache format (KVATTN_FP16, KVATTN_FMT).
+// Paged attention for few rows (up to 16 of a sequence and kv head): compiled once
+// per source type and cache format (KVATTN_FP16, KVATTN_FMT).
 //
 //   out = sum_k softmax_k(c q . K_k) V_k over the keys that a row sees.
 //
